@@ -36,6 +36,7 @@ BLOCK = {"mxfp4": 32, "nvfp4": 16, "int4": 32}
 
 _i, _f, _p, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 _fp = ctypes.POINTER(ctypes.c_float)
+_l = ctypes.c_int64
 
 _SIGS = {
     "wush_format_block": ([_i], _i),
@@ -72,6 +73,20 @@ _SIGS = {
     "wush_had256_gemv_ws_bytes": ([_i, _i], _sz),
     "wush_had256_gemv": ([_i, _i, _i, _p, _p, _p, _p, _sz, _p], _i),
     "wush_had256_rotate": ([_i, _i, _p, _p, _p], _i),
+    "wush_block_norm": ([_i, _i, _i, _i, _i, _p, _p, _i, _p, _f, _p, _f, _p, _f, _p, _p, _p, _p, _p], _i),
+    "wush_block_norm_bwd_ws_bytes": ([_i, _i], _sz),
+    "wush_block_norm_bwd": ([_i, _i, _i, _i, _i, _p, _p, _p, _p, _i, _p, _f, _p, _f, _p, _p, _p, _p, _p, _p, _p, _p,
+                             _p, _sz, _p], _i),
+    "wush_act8_pack": ([_i, _i, _i, _p, _p, _p, _p], _i),
+    "wush_act8_unpack": ([_i, _i, _i, _p, _p, _p, _p], _i),
+    "wush_act8_swiglu": ([_i, _i, _i, _i, _p, _p, _l, _p, _p, _p, _p, _p, _p], _i),
+    "wush_act8_swiglu_bwd": ([_i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _l, _p], _i),
+    "wush_adapter_ws_bytes": ([_i, _i, _i, _i], _sz),
+    "wush_adapter_forward": ([_i, _i, _i, _i, _i, _p, _l, _i, _p, _p, _i, _i, _p, _p, _p, _p, _p, _l, _p, _l, _p, _p,
+                              _sz, _p], _i),
+    "wush_adapter_backward_ws_bytes": ([_i, _i, _i, _i, _i, _i], _sz),
+    "wush_adapter_backward": ([_i, _i, _i, _i, _i, _i, _p, _l, _p, _p, _l, _i, _p, _p, _i, _i, _p, _p, _p, _p, _p, _p,
+                               _l, _p, _l, _p, _p, _p, _sz, _p], _i),
     "wush_status_string": ([_i], ctypes.c_char_p),
     "wush_last_error": ([], ctypes.c_char_p),
     "wush_version": ([], ctypes.c_char_p),
@@ -391,6 +406,246 @@ def wush_had256_gemv(x, packed, y, ws=None, stream=None):
 def wush_had256_rotate(inp, out, stream=None):
     rows, d_in = inp.shape
     _check(lib.wush_had256_rotate(rows, d_in, _ptr(inp), _ptr(out), _stream(stream)), "wush_had256_rotate")
+
+
+# ----------------------------------------------------------------------------- around a frozen projection
+
+GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _dt(t, name):
+    """wush_dtype of a float32 or bfloat16 tensor."""
+    code = _FLOATS.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32 or bfloat16, not %s" % (name, t.dtype))
+    return code
+
+
+def _want(t, name, shape, dtype=None):
+    """A contiguous tensor of that shape (and dtype), or an exception."""
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _rows(t, name, n, d):
+    """Row stride of an [n][d] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != d:
+        raise ValueError("%s must have shape (%d, %d), not %s" % (name, n, d, tuple(t.shape)))
+    if t.stride(1) != 1 and d > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.stride(0) if n > 1 else d
+
+
+def _gate(gate, n, d, ydt):
+    """Kind of a gate by its shape: [d] per channel, [n][1] per token, [n][d] per element."""
+    if gate is None:
+        return 0
+    if gate.dim() == 1:
+        _want(gate, "gate", (d,), torch.float32)
+        return 1
+    if tuple(gate.shape) == (n, 1) and d != 1:
+        _want(gate, "gate", (n, 1), torch.float32)
+        return 2
+    _want(gate, "gate", (n, d), ydt)
+    return 3
+
+
+def wush_block_norm(Y, w_post, gate, R, w_pre, Rout, U, rstd_post=None, rstd_pre=None, branch_scale=1.0, res_scale=1.0,
+                    eps=1e-6, stream=None):
+    """Rout = res_scale R + branch_scale gate norm(Y) w_post; U = norm(Rout) w_pre.  Y, w_post, gate, w_pre with U, and
+    Rout may be None; gate is [d], [n][1] (float32) or [n][d] (Y's dtype)."""
+    n, d = R.shape
+    _want(R, "R", (n, d))
+    if Y is not None:
+        _want(Y, "Y", (n, d))
+    if Rout is not None:
+        _want(Rout, "Rout", (n, d), R.dtype)
+    if U is not None:
+        _want(U, "U", (n, d))
+    for t, name, size in ((w_post, "w_post", d), (w_pre, "w_pre", d), (rstd_post, "rstd_post", n),
+                          (rstd_pre, "rstd_pre", n)):
+        if t is not None:
+            _want(t, name, (size,), torch.float32)
+    kind = _gate(gate, n, d, None if Y is None else Y.dtype)
+    rdt = _dt(R, "R")
+    ydt = rdt if Y is None else _dt(Y, "Y")
+    udt = rdt if U is None else _dt(U, "U")
+    _check(lib.wush_block_norm(ydt, rdt, udt, n, d, _ptr(Y), _ptr(w_post), kind, _ptr(gate), branch_scale, _ptr(R),
+                               res_scale, _ptr(w_pre), eps, _ptr(Rout), _ptr(U), _ptr(rstd_post), _ptr(rstd_pre),
+                               _stream(stream)), "wush_block_norm")
+
+
+def wush_block_norm_bwd_ws_bytes(n, d):
+    return lib.wush_block_norm_bwd_ws_bytes(n, d)
+
+
+def wush_block_norm_bwd(dU, dRout, Y, w_post, gate, Rout, w_pre, rstd_post, rstd_pre, dY, dR, dgate, dw_post, dw_pre,
+                        branch_scale=1.0, res_scale=1.0, ws=None, stream=None):
+    """Gradients of wush_block_norm; dU (with w_pre and dw_pre) or dRout may be None, and so may dR."""
+    some = next((t for t in (Rout, dRout, Y) if t is not None), None)
+    if some is None:
+        raise ValueError("wush_block_norm_bwd needs Rout, dRout or Y")
+    n, d = some.shape
+    rdts = {t.dtype for t in (Rout, dRout, dR) if t is not None}
+    if len(rdts) > 1:
+        raise TypeError("Rout, dRout and dR must have one dtype")
+    for t, name in ((Rout, "Rout"), (dRout, "dRout"), (dR, "dR"), (dU, "dU")):
+        if t is not None:
+            _want(t, name, (n, d))
+    if Y is not None:
+        _want(Y, "Y", (n, d))
+        if dY is not None:
+            _want(dY, "dY", (n, d), Y.dtype)
+    for t, name, size in ((w_post, "w_post", d), (w_pre, "w_pre", d), (dw_post, "dw_post", d), (dw_pre, "dw_pre", d),
+                          (rstd_post, "rstd_post", n), (rstd_pre, "rstd_pre", n)):
+        if t is not None:
+            _want(t, name, (size,), torch.float32)
+    kind = _gate(gate, n, d, None if Y is None else Y.dtype)
+    if gate is not None and dgate is not None:
+        _want(dgate, "dgate", tuple(gate.shape), gate.dtype)
+    first = next((t for t in (Rout, dRout, dR) if t is not None), None)
+    rdt = 0 if first is None else _dt(first, "Rout")
+    ydt = rdt if Y is None else _dt(Y, "Y")
+    udt = rdt if dU is None else _dt(dU, "dU")
+    wp, wb = _ws(ws)
+    _check(lib.wush_block_norm_bwd(ydt, rdt, udt, n, d, _ptr(dU), _ptr(dRout), _ptr(Y), _ptr(w_post), kind, _ptr(gate),
+                                   branch_scale, _ptr(Rout), res_scale, _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre),
+                                   _ptr(dY), _ptr(dR), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), wp, wb,
+                                   _stream(stream)), "wush_block_norm_bwd")
+
+
+def _checkpoint(codes, scales, n, d, name):
+    _want(codes, name + " codes", (n, d), torch.int8)
+    _want(scales, name + " scales", (n, d // 32), torch.uint8)
+
+
+def wush_act8_pack(X, codes, scales, stream=None):
+    """X: device [n][d] float32 or bfloat16 -> codes int8 [n][d], scales uint8 [n][d/32]."""
+    n, d = X.shape
+    _want(X, "X", (n, d))
+    _checkpoint(codes, scales, n, d, "act8")
+    _check(lib.wush_act8_pack(_dt(X, "X"), n, d, _ptr(X), _ptr(codes), _ptr(scales), _stream(stream)),
+           "wush_act8_pack")
+
+
+def wush_act8_unpack(codes, scales, Y, stream=None):
+    """The values of a checkpoint, to Y: device [n][d] float32 or bfloat16."""
+    n, d = Y.shape
+    _want(Y, "Y", (n, d))
+    _checkpoint(codes, scales, n, d, "act8")
+    _check(lib.wush_act8_unpack(_dt(Y, "Y"), n, d, _ptr(codes), _ptr(scales), _ptr(Y), _stream(stream)),
+           "wush_act8_unpack")
+
+
+def _pair(a, b, name_a, name_b, n, d):
+    """Common row stride and dtype of two [n][d] tensors."""
+    ld = _rows(a, name_a, n, d)
+    if _rows(b, name_b, n, d) != ld or a.dtype != b.dtype:
+        raise ValueError("%s and %s must have one dtype and row stride" % (name_a, name_b))
+    return ld
+
+
+def wush_act8_swiglu(G, U, H, g_codes=None, g_scales=None, u_codes=None, u_scales=None, stream=None):
+    """H = G sigmoid(G) U, keeping G and U as act8 checkpoints where their four tensors are given.  G and U may be the
+    halves of one tensor (rows contiguous, one row stride)."""
+    n, d = G.shape
+    ld = _pair(G, U, "G", "U", n, d)
+    _want(H, "H", (n, d))
+    if g_codes is not None and g_scales is not None:
+        _checkpoint(g_codes, g_scales, n, d, "G")
+    if u_codes is not None and u_scales is not None:
+        _checkpoint(u_codes, u_scales, n, d, "U")
+    _check(lib.wush_act8_swiglu(_dt(G, "G"), _dt(H, "H"), n, d, _ptr(G), _ptr(U), ld, _ptr(H), _ptr(g_codes),
+                                _ptr(g_scales), _ptr(u_codes), _ptr(u_scales), _stream(stream)), "wush_act8_swiglu")
+
+
+def wush_act8_swiglu_bwd(dH, g_codes, g_scales, u_codes, u_scales, dG, dU, stream=None):
+    """Gradients of wush_act8_swiglu at the checkpoints' values; dG and dU may be the halves of one tensor."""
+    n, d = dH.shape
+    _want(dH, "dH", (n, d))
+    ld = _pair(dG, dU, "dG", "dU", n, d)
+    _checkpoint(g_codes, g_scales, n, d, "G")
+    _checkpoint(u_codes, u_scales, n, d, "U")
+    _check(lib.wush_act8_swiglu_bwd(_dt(dH, "dH"), _dt(dG, "dG"), n, d, _ptr(dH), _ptr(g_codes), _ptr(g_scales),
+                                    _ptr(u_codes), _ptr(u_scales), _ptr(dG), _ptr(dU), ld, _stream(stream)),
+           "wush_act8_swiglu_bwd")
+
+
+def _adapters(seg_off, seg_adapter, A, Bt, rank, alpha):
+    """(nseg, nad, rmax, d_in, d_out) of a set of adapters and the requests that use it."""
+    nad, rmax, d_in = A.shape
+    d_out = Bt.shape[-1]
+    nseg = seg_adapter.shape[0]
+    _want(A, "A", (nad, rmax, d_in), torch.bfloat16)
+    _want(Bt, "Bt", (nad, rmax, d_out), torch.bfloat16)
+    _want(seg_off, "seg_off", (nseg + 1,), torch.int32)
+    _want(seg_adapter, "seg_adapter", (nseg,), torch.int32)
+    _want(rank, "rank", (nad,), torch.int32)
+    _want(alpha, "alpha", (nad,), torch.float32)
+    return nseg, nad, rmax, d_in, d_out
+
+
+def wush_adapter_ws_bytes(n, d_in, nseg, rmax):
+    return lib.wush_adapter_ws_bytes(n, d_in, nseg, rmax)
+
+
+def wush_adapter_forward(X, seg_off, seg_adapter, A, Bt, rank, alpha, Y0, Y, V=None, ws=None, stream=None):
+    """Y = Y0 + V Bt with V = alpha X A^T, each request with its adapter (device int32 seg_off [nseg+1], seg_adapter
+    [nseg], -1 for none).  A, Bt: bfloat16 [nad][rmax][d]; rank int32, alpha float32 [nad].  X, Y0 (or None) and Y are
+    float32 or bfloat16 with contiguous rows; V float32 [n][rmax] is kept for the backward call where given."""
+    nseg, nad, rmax, d_in, d_out = _adapters(seg_off, seg_adapter, A, Bt, rank, alpha)
+    n = X.shape[0]
+    ldx, ldy = _rows(X, "X", n, d_in), _rows(Y, "Y", n, d_out)
+    ldy0 = d_out
+    if Y0 is not None:
+        ldy0 = _rows(Y0, "Y0", n, d_out)
+        if Y0.dtype != Y.dtype:
+            raise TypeError("Y0 and Y must have one dtype")
+    if V is not None:
+        _want(V, "V", (n, rmax), torch.float32)
+    wp, wb = _ws(ws)
+    _check(lib.wush_adapter_forward(_dt(X, "X"), _dt(Y, "Y"), n, d_in, d_out, _ptr(X), ldx, nseg, _ptr(seg_off),
+                                    _ptr(seg_adapter), nad, rmax, _ptr(A), _ptr(Bt), _ptr(rank), _ptr(alpha), _ptr(Y0),
+                                    ldy0, _ptr(Y), ldy, _ptr(V), wp, wb, _stream(stream)), "wush_adapter_forward")
+
+
+def wush_adapter_backward_ws_bytes(n, d_in, d_out, nseg, nad, rmax):
+    return lib.wush_adapter_backward_ws_bytes(n, d_in, d_out, nseg, nad, rmax)
+
+
+def wush_adapter_backward(dY, X, seg_off, seg_adapter, A, Bt, rank, alpha, V, dX0, dX, dA, dBt, x_scales=None, ws=None,
+                          stream=None):
+    """dX = dX0 + dV A, dA = dV^T X and dBt = V^T dY (float32, shaped like A and Bt) with dV = alpha dY Bt^T.  X: as in
+    the forward call, or the int8 codes of its act8 checkpoint with x_scales.  dX0 may be None (zeros), dX too."""
+    nseg, nad, rmax, d_in, d_out = _adapters(seg_off, seg_adapter, A, Bt, rank, alpha)
+    n = dY.shape[0]
+    ldg = _rows(dY, "dY", n, d_out)
+    if x_scales is not None:
+        _checkpoint(X, x_scales, n, d_in, "X")
+        ldx, xdt = d_in, 1
+    else:
+        ldx, xdt = _rows(X, "X", n, d_in), _dt(X, "X")
+    _want(V, "V", (n, rmax), torch.float32)
+    _want(dA, "dA", (nad, rmax, d_in), torch.float32)
+    _want(dBt, "dBt", (nad, rmax, d_out), torch.float32)
+    ldd0 = ldd = d_in
+    ydt = 1
+    if dX is not None:
+        ldd, ydt = _rows(dX, "dX", n, d_in), _dt(dX, "dX")
+    if dX0 is not None:
+        ldd0 = _rows(dX0, "dX0", n, d_in)
+        if dX is None or dX0.dtype != dX.dtype:
+            raise TypeError("dX0 and dX must have one dtype")
+    wp, wb = _ws(ws)
+    _check(lib.wush_adapter_backward(_dt(dY, "dY"), xdt, ydt, n, d_in, d_out, _ptr(dY), ldg, _ptr(X), _ptr(x_scales),
+                                     ldx, nseg, _ptr(seg_off), _ptr(seg_adapter), nad, rmax, _ptr(A), _ptr(Bt),
+                                     _ptr(rank), _ptr(alpha), _ptr(V), _ptr(dX0), ldd0, _ptr(dX), ldd, _ptr(dA),
+                                     _ptr(dBt), wp, wb, _stream(stream)), "wush_adapter_backward")
 
 
 def wush_version():

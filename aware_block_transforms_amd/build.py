@@ -22,7 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwush.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
-HIP_SOURCES = ["transform_quant.hip", "gemm_mxfp4.hip", "gemm_nv_int4.hip", "gemm_nvfp4.hip", "gemm_int4.hip", "gemm.hip", "loss.hip", "had256.hip", "moments.hip", "builder_dev.hip"]
+HIP_SOURCES = ["transform_quant.hip", "gemm_mxfp4.hip", "gemm_nv_int4.hip", "gemm_nvfp4.hip", "gemm_int4.hip", "gemm.hip", "loss.hip", "had256.hip", "moments.hip", "builder_dev.hip",
+               "norm.hip", "act8.hip", "adapter.hip", "adapter_grad.hip"]
 # matrix-core ceiling probes for bench.py: their own library, none of the method's arithmetic
 CEILING_SOURCE = "ceiling.hip"
 CEILING_LIB = os.path.join(PKG, "libwush_ceiling.so")

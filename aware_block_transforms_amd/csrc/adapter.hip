@@ -1,0 +1,546 @@
+// Low-rank adapters of many requests beside a shared projection.
+//
+// Adapter a has A [R][d_in] and Bt [R][d_out] (the transpose of the usual B),
+// of which the first rank[a] rows count, and a factor alpha[a].  For the tokens
+// of a request with adapter a
+//   V = alpha X A^T,   Y = Y0 + V Bt,
+// and backward, from dY and the V of the forward call,
+//   dV = alpha dY Bt^T,   dX = dX0 + dV A,   dA = dV^T X,   dBt = V^T dY.
+// With both factors stored as rows of d values, three kernels do all of it:
+//   low     V  = alpha X A^T   (also dV from dY and Bt)
+//   spread  Y  = Y0 + V Bt     (also dX from dV and A)
+//   grad    dA = dV^T X        (also dBt from V and dY), in adapter_grad.hip
+// All are bound by HBM at ranks up to 64: a rank-r pass does r flops per byte
+// of X, against a matrix rate of some 300 per byte of bandwidth.  So X, Y0, Y
+// and dY stream once, straight from memory into matrix operands, and the
+// operands of fp32 values are split into three bf16 terms (split3), which
+// keeps V and all results at fp32 accuracy.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "adapter.h"
+#include "common.h"
+
+using namespace wush;
+
+namespace wush {
+wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int d_in, int d_out, const void* dY,
+                          int64_t ldg, const void* X, const uint8_t* x_scales, int64_t ldx, int nseg,
+                          const int* seg_off, const int* seg_adapter, int nad, int rmax, const int* rank,
+                          const float* V, const float* dV, float* dA, float* dBt, void* ws, hipStream_t s);
+bool adapter_grads_fit(int n, int d_in, int d_out, int nad);
+size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax);
+}  // namespace wush
+
+namespace {
+
+constexpr int kWaves = 4;
+
+// ---------------------------------------------------------------------------
+// low: V[t][r] = alpha sum_k X[t][k] A[r][k], by 16x16x32 products of token
+// rows with factor rows, both read with k along the row.  A workgroup takes
+// 16 TT tokens; its four waves and the grid's y share k in pieces of 64, each
+// lane 16 neighbouring values of a row (two products; which k a lane holds
+// does not matter as long as both operands agree).  The waves' sums are joined
+// through LDS, those of the y workgroups lie in `part` [gridDim.y][n][R] and
+// are added by whoever reads V.  Rows past the tile's tokens or the rank
+// repeat the last one, so no load needs a guard; their results are dropped.
+
+template <class T>
+struct XOps;
+template <>
+struct XOps<bf16_t> {
+  static constexpr int kTerms = 1;
+  u32x4 v[2];
+  __device__ __forceinline__ void load(const bf16_t* p) {
+    v[0] = reinterpret_cast<const u32x4*>(p)[0];
+    v[1] = reinterpret_cast<const u32x4*>(p)[1];
+  }
+  __device__ __forceinline__ void load_tail(const bf16_t* p, int left) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h] = left > 8 * h ? reinterpret_cast<const u32x4*>(p)[h] : u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void operand(int h, u32x4 (&t)[3]) const { t[0] = v[h]; }
+};
+template <>
+struct XOps<float> {
+  static constexpr int kTerms = 3;
+  f32x4 v[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) v[h] = reinterpret_cast<const f32x4*>(p)[h];
+  }
+  __device__ __forceinline__ void load_tail(const float* p, int left) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      v[h] = left > 4 * h ? reinterpret_cast<const f32x4*>(p)[h] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  __device__ __forceinline__ void operand(int h, u32x4 (&t)[3]) const {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = v[2 * h][i];
+      x[4 + i] = v[2 * h + 1][i];
+    }
+    split8(x, t);
+  }
+};
+
+template <class X, int RT, int TT>
+__global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, const X* __restrict__ x, int64_t ldx,
+                                                                  int nseg, const int* __restrict__ off,
+                                                                  const int* __restrict__ ids, int nad,
+                                                                  const bf16_t* __restrict__ factor,
+                                                                  const int* __restrict__ rank,
+                                                                  const float* __restrict__ alpha,
+                                                                  float* __restrict__ part) {
+  constexpr int R = 16 * RT, T = 16 * TT;
+  __shared__ float red[kWaves][T * R];
+  const Tile t = find_tile<T>(blockIdx.x, n, nseg, off, ids, nad);
+  if (t.begin >= t.end) return;
+  float* out = part + (static_cast<int64_t>(blockIdx.y) * n + t.begin) * R;
+  const int rows = t.end - t.begin;
+  const int rk = t.adapter < 0 ? 0 : min(max(rank[t.adapter], 0), R);
+  if (rk == 0) {
+    for (int i = threadIdx.x; i < rows * R; i += 64 * kWaves) out[i] = 0.0f;
+    return;
+  }
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const X* xp[TT];
+  const bf16_t* fp[RT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) xp[i] = x + static_cast<int64_t>(min(t.begin + 16 * i + j, t.end - 1)) * ldx + 16 * g;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    fp[i] = factor + (static_cast<int64_t>(t.adapter) * R + min(16 * i + j, rk - 1)) * d + 16 * g;
+  f32x4 acc[TT][RT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[i][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int tiles = (rk + 15) / 16;   // row tiles in use
+  const int step = 64 * kWaves * gridDim.y;
+  auto multiply = [&](const XOps<X>(&xo)[TT], const XOps<bf16_t>(&fo)[RT]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 xt[TT][3];
+#pragma unroll
+      for (int i = 0; i < TT; ++i) xo[i].operand(h, xt[i]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (r >= tiles) break;
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int m = 0; m < XOps<X>::kTerms; ++m) acc[i][r] = mfma(xt[i][m], fo[r].v[h], acc[i][r]);
+      }
+    }
+  };
+  int k = 64 * (kWaves * blockIdx.y + wave);
+  for (; k + 64 <= d; k += step) {
+    XOps<X> xo[TT];
+    XOps<bf16_t> fo[RT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) xo[i].load(xp[i] + k);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (r < tiles) fo[r].load(fp[r] + k);
+    multiply(xo, fo);
+  }
+  if (k < d) {
+    XOps<X> xo[TT];
+    XOps<bf16_t> fo[RT];
+    const int left = d - k - 16 * g;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) xo[i].load_tail(xp[i] + k, left);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (r < tiles) fo[r].load_tail(fp[r] + k, left);
+    multiply(xo, fo);
+  }
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][(16 * i + 4 * g + e) * R + 16 * r + j] = acc[i][r][e];
+  __syncthreads();
+  const float f = alpha[t.adapter];
+  for (int i = threadIdx.x; i < rows * R; i += 64 * kWaves) {
+    float s = red[0][i];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += red[w][i];
+    out[i] = i % R < rk ? f * s : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// spread: Y[t][c] = Y0[t][c] + sum_r V[t][r] Bt[r][c].  A wave owns 16 CW
+// columns: its lane j those from CW j on, so that a row of Y0 and Y is read and
+// written in whole 256-byte runs, 16 bytes a lane.  The factor's rows lie along
+// the columns, so a lane reads eight rows (k) of its CW columns and exchanges
+// halves between them to get CW operands; they stay in registers while the
+// workgroup walks over its 16 TT tokens.  The sums start from Y0.
+
+template <class T>
+struct YRow;
+template <>
+struct YRow<float> {
+  static constexpr int CW = 4;
+  using raw = f32x4;
+  using factors = u32x2;
+  f32x4 v;
+  __device__ __forceinline__ float at(int c) const { return v[c]; }
+  __device__ __forceinline__ void put(const float* s) { v = f32x4{s[0], s[1], s[2], s[3]}; }
+};
+template <>
+struct YRow<bf16_t> {
+  static constexpr int CW = 8;
+  using raw = u32x4;
+  using factors = u32x4;
+  u32x4 v;
+  __device__ __forceinline__ float at(int c) const {
+    return __builtin_bit_cast(float, c & 1 ? v[c / 2] & 0xffff0000u : v[c / 2] << 16);
+  }
+  __device__ __forceinline__ void put(const float* s) {
+    v = u32x4{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]), pack_bf16(s[6], s[7])};
+  }
+};
+
+template <class Y, int RT, int TT>
+__global__ __launch_bounds__(64 * kWaves) void adapter_spread_kernel(int n, int d, int col_wgs,
+                                                                     const float* __restrict__ part, int splits,
+                                                                     int nseg,
+                                                                     const int* __restrict__ off,
+                                                                     const int* __restrict__ ids, int nad,
+                                                                     const bf16_t* __restrict__ factor,
+                                                                     const int* __restrict__ rank, const Y* y0,
+                                                                     int64_t ld0, Y* y, int64_t ldy,
+                                                                     float* __restrict__ V) {
+  constexpr int R = 16 * RT, T = 16 * TT, KS = (R + 31) / 32, CW = YRow<Y>::CW;
+  using raw = typename YRow<Y>::raw;
+  const int col_wg = blockIdx.x % col_wgs;
+  const Tile t = find_tile<T>(blockIdx.x / col_wgs, n, nseg, off, ids, nad);
+  if (t.begin >= t.end) return;
+  const int rows = t.end - t.begin;
+  const int64_t v_step = static_cast<int64_t>(n) * R;
+  // V itself, where the caller keeps it: the first column workgroup writes it
+  if (V && col_wg == 0) {
+    const int64_t b = static_cast<int64_t>(t.begin) * R;
+    for (int i = threadIdx.x; i < rows * R; i += 64 * kWaves) {
+      float s = part[b + i];
+      for (int p = 1; p < splits; ++p) s += part[b + p * v_step + i];
+      V[b + i] = s;
+    }
+  }
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c0 = (col_wg * kWaves + wave) * 16 * CW;
+  if (c0 >= d) return;
+  // lanes past the last column repeat it and store nothing: the matrix
+  // instructions take their token rows from every lane
+  const bool in_c = c0 + CW * j < d;
+  const int c = in_c ? c0 + CW * j : d - CW;
+  const int rk = t.adapter < 0 ? 0 : min(max(rank[t.adapter], 0), R);
+  u32x4 w[KS][CW];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    if (32 * ks >= rk) {
+#pragma unroll
+      for (int i = 0; i < CW; ++i) w[ks][i] = u32x4{0u, 0u, 0u, 0u};
+      continue;
+    }
+    typename YRow<Y>::factors in[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = min(32 * ks + 8 * g + i, rk - 1);
+      in[i] = *reinterpret_cast<const typename YRow<Y>::factors*>(
+          factor + (static_cast<int64_t>(t.adapter) * R + r) * d + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int q = 0; q < CW / 2; ++q)
+        if (32 * ks + 8 * g + i >= rk) in[i][q] = 0u;
+#pragma unroll
+    for (int i = 0; i < CW; ++i)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        w[ks][i][p] = __builtin_amdgcn_perm(in[2 * p + 1][i / 2], in[2 * p][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+  }
+  for (int i = 0; i < TT; ++i) {
+    if (16 * i >= rows) break;
+    YRow<Y> in[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t row = min(t.begin + 16 * i + 4 * g + e, t.end - 1);
+      if (y0)
+        in[e].v = *reinterpret_cast<const raw*>(y0 + row * ld0 + c);
+      else
+        in[e].v = raw{0, 0, 0, 0};
+    }
+    f32x4 acc[CW];
+#pragma unroll
+    for (int q = 0; q < CW; ++q) acc[q] = f32x4{in[0].at(q), in[1].at(q), in[2].at(q), in[3].at(q)};
+    if (rk > 0) {
+      const float* vp = part + static_cast<int64_t>(min(t.begin + 16 * i + j, t.end - 1)) * R + 8 * g;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (32 * ks >= rk) break;
+        float v[8];
+        const bool in_r = 32 * ks + 8 * g < R;
+        raw8<float> r;
+        load8(r, vp + (in_r ? 32 * ks : -8 * g));
+        widen8(r, v);
+        for (int p = 1; p < splits; ++p) {
+          float o[8];
+          load8(r, vp + p * v_step + (in_r ? 32 * ks : -8 * g));
+          widen8(r, o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] += o[q];
+        }
+        if (!in_r) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+        }
+        u32x4 vt[3];
+        split8(v, vt);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int q = 0; q < CW; ++q) acc[q] = mfma(vt[m], w[ks][q], acc[q]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = t.begin + 16 * i + 4 * g + e;
+      float s[CW];
+#pragma unroll
+      for (int q = 0; q < CW; ++q) s[q] = acc[q][e];
+      YRow<Y> o;
+      o.put(s);
+      if (in_c && row < t.end) *reinterpret_cast<raw*>(y + row * ldy + c) = o.v;
+    }
+  }
+}
+
+// V = the sum of the low kernel's parts, where no spread kernel writes it.
+__global__ __launch_bounds__(256) void adapter_sum_kernel(int64_t count, const float* __restrict__ part, int splits,
+                                                          float* __restrict__ V) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= count) return;
+  float s = part[i];
+  for (int p = 1; p < splits; ++p) s += part[p * count + i];
+  V[i] = s;
+}
+
+// Token tiles of the low kernel: as many rows as the average request fills, so
+// that the factor's rows are read once for them; at most 64, 32 at rank 128
+// (the sums take 64 registers per lane at either limit).
+int low_tiles(int n, int nseg, int rmax) {
+  const int avg = n / (nseg > 0 ? nseg : 1);
+  const int most = rmax > 64 ? 2 : 4;
+  const int want = avg > 32 ? 4 : avg > 16 ? 2 : 1;
+  return want < most ? want : most;
+}
+
+// Tokens a spread workgroup walks over: 64, so that the factor's operands are
+// built once for four tiles; 16 where requests are short.
+bool short_requests(int n, int nseg) { return n / nseg <= 16; }
+
+// Workgroups along k: four for every compute unit over the whole grid, while
+// each of their waves still has a piece of 64 values of its own.
+int low_splits(int n, int d, int nseg, int rmax) {
+  const int64_t tiles = tile_numbers(n, 16 * low_tiles(n, nseg, rmax), nseg);
+  const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves);
+  int s = static_cast<int>((1024 + tiles - 1) / tiles);
+  if (s > 16) s = 16;
+  if (s > pieces) s = pieces;
+  return s < 1 ? 1 : s;
+}
+
+template <class X, int RT>
+void low_by_tiles(int tt, int splits, int n, int d, const void* x, int64_t ldx, int nseg, const int* off,
+                  const int* ids, int nad, const void* factor, const int* rank, const float* alpha, float* part,
+                  hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(tile_numbers(n, 16 * tt, nseg)), splits);
+  auto k = adapter_low_kernel<X, RT, 1>;
+  if (tt == 2) k = adapter_low_kernel<X, RT, 2>;
+  if (tt == 4) k = adapter_low_kernel<X, RT, RT == 8 ? 2 : 4>;
+  hipLaunchKernelGGL(k, grid, dim3(64 * kWaves), 0, s, n, d, static_cast<const X*>(x), ldx, nseg, off, ids, nad,
+                     static_cast<const bf16_t*>(factor), rank, alpha, part);
+}
+
+template <class X>
+void low(int n, int d, const void* x, int64_t ldx, int nseg, const int* off, const int* ids, int nad, int rmax,
+         const void* factor, const int* rank, const float* alpha, float* part, hipStream_t s) {
+  auto f = rmax == 16 ? low_by_tiles<X, 1> : rmax == 32 ? low_by_tiles<X, 2> : rmax == 64 ? low_by_tiles<X, 4>
+                                                                                         : low_by_tiles<X, 8>;
+  f(low_tiles(n, nseg, rmax), low_splits(n, d, nseg, rmax), n, d, x, ldx, nseg, off, ids, nad, factor, rank, alpha,
+    part, s);
+}
+
+template <class Y, int RT>
+void spread_by_tiles(bool one, int n, int d, const float* part, int splits, int nseg, const int* off, const int* ids,
+                     int nad, const void* factor, const int* rank, const void* y0, int64_t ld0, void* y, int64_t ldy,
+                     float* V, hipStream_t s) {
+  const int cols = 16 * YRow<Y>::CW * kWaves, tokens = one ? 16 : 64;
+  const int col_wgs = (d + cols - 1) / cols;
+  const dim3 grid(static_cast<unsigned>(col_wgs * tile_numbers(n, tokens, nseg)));
+  auto k = one ? adapter_spread_kernel<Y, RT, 1> : adapter_spread_kernel<Y, RT, 4>;
+  hipLaunchKernelGGL(k, grid, dim3(64 * kWaves), 0, s, n, d, col_wgs, part, splits, nseg, off, ids, nad,
+                     static_cast<const bf16_t*>(factor), rank, static_cast<const Y*>(y0), ld0, static_cast<Y*>(y), ldy,
+                     V);
+}
+
+template <class Y>
+void spread(int n, int d, const float* part, int splits, int nseg, const int* off, const int* ids, int nad, int rmax,
+            const void* factor, const int* rank, const void* y0, int64_t ld0, void* y, int64_t ldy, float* V,
+            hipStream_t s) {
+  auto f = rmax == 16 ? spread_by_tiles<Y, 1> : rmax == 32 ? spread_by_tiles<Y, 2>
+                                              : rmax == 64 ? spread_by_tiles<Y, 4> : spread_by_tiles<Y, 8>;
+  f(short_requests(n, nseg), n, d, part, splits, nseg, off, ids, nad, factor, rank, y0, ld0, y, ldy, V, s);
+}
+
+bool rank_ok(int rmax) { return rmax == 16 || rmax == 32 || rmax == 64 || rmax == 128; }
+
+size_t part_bytes(int n, int d, int nseg, int rmax) {
+  return static_cast<size_t>(low_splits(n, d, nseg, rmax)) * n * rmax * sizeof(float);
+}
+
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+constexpr int kMaxSeg = 1 << 20;
+constexpr int kMaxTokens = 1 << 24;   // so that sums over 64 requests stay in 32 bits
+
+// X as the grad kernel sees it: the two float types and the act8 codes.
+constexpr int kAct8 = 2;
+
+wush_status check(const char* who, wush_dtype a, wush_dtype b, wush_dtype c, int n, int d_in, int d_out, int nseg,
+                  int nad, int rmax) {
+  for (wush_dtype t : {a, b, c})
+    if (t != WUSH_F32 && t != WUSH_BF16) return fail(WUSH_E_ARG, "%s: bad dtype", who);
+  if (n < 0 || n > kMaxTokens || d_in < 8 || d_in % 8 || d_out < 8 || d_out % 8)
+    return fail(WUSH_E_SHAPE, "%s: need n in 0..%d and d_in, d_out positive multiples of 8 (n=%d d_in=%d d_out=%d)", who,
+                kMaxTokens, n, d_in, d_out);
+  if (!rank_ok(rmax)) return fail(WUSH_E_SHAPE, "%s: rmax must be 16, 32, 64 or 128 (got %d)", who, rmax);
+  if (nad < 1 || nseg < 1 || nseg > kMaxSeg)
+    return fail(WUSH_E_SHAPE, "%s: need at least one adapter and 1..%d requests (nad=%d nseg=%d)", who, kMaxSeg, nad, nseg);
+  const int64_t d = d_in > d_out ? d_in : d_out;
+  if (tile_numbers(n, short_requests(n, nseg) ? 16 : 64, nseg) * ((d + 255) / 256) > 0x7fffffff)
+    return fail(WUSH_E_SHAPE, "%s: n=%d with nseg=%d passes the launch limit", who, n, nseg);
+  return WUSH_OK;
+}
+
+wush_status launched(const char* who) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? WUSH_OK : fail(WUSH_E_HIP, "%s launch: %s", who, hipGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" size_t wush_adapter_ws_bytes(int n, int d_in, int nseg, int rmax) {
+  if (n < 1 || n > kMaxTokens || d_in < 8 || d_in % 8 || nseg < 1 || nseg > kMaxSeg || !rank_ok(rmax)) return 0;
+  return part_bytes(n, d_in, nseg, rmax);
+}
+
+extern "C" wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int n, int d_in, int d_out, const void* X,
+                                            int64_t ldx, int nseg, const int* seg_off, const int* seg_adapter, int nad,
+                                            int rmax, const void* A, const void* Bt, const int* rank,
+                                            const float* alpha, const void* Y0, int64_t ldy0, void* Y, int64_t ldy,
+                                            float* V, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "wush_adapter_forward";
+  const wush_status st = check(who, xdt, ydt, ydt, n, d_in, d_out, nseg, nad, rmax);
+  if (st != WUSH_OK) return st;
+  if (ldx < d_in || ldx % 8 || ldy < d_out || ldy % 8 || (Y0 && (ldy0 < d_out || ldy0 % 8)))
+    return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
+  if (n == 0) return WUSH_OK;
+  if (!X || !seg_off || !seg_adapter || !A || !Bt || !rank || !alpha || !Y) return fail(WUSH_E_ARG, "%s: null pointer", who);
+  for (const void* p : {X, A, Bt, Y0, static_cast<const void*>(Y), static_cast<const void*>(V), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  const size_t need = part_bytes(n, d_in, nseg, rmax);
+  if (ws && ws_bytes < need) return fail(WUSH_E_ARG, "%s: workspace of %zu bytes, need %zu", who, ws_bytes, need);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* part = static_cast<float*>(ws);
+  if (!ws) {
+    const hipError_t e = hipMallocAsync(reinterpret_cast<void**>(&part), need, s);
+    if (e != hipSuccess) return fail(WUSH_E_HIP, "%s: scratch: %s", who, hipGetErrorString(e));
+  }
+  auto f = xdt == WUSH_F32 ? low<float> : low<bf16_t>;
+  f(n, d_in, X, ldx, nseg, seg_off, seg_adapter, nad, rmax, A, rank, alpha, part, s);
+  wush_status out = launched(who);
+  if (out == WUSH_OK) {
+    auto g = ydt == WUSH_F32 ? spread<float> : spread<bf16_t>;
+    g(n, d_out, part, low_splits(n, d_in, nseg, rmax), nseg, seg_off, seg_adapter, nad, rmax, Bt, rank, Y0, ldy0, Y,
+      ldy, V, s);
+    out = launched(who);
+  }
+  if (!ws) (void)hipFreeAsync(part, s);
+  return out;
+}
+
+extern "C" size_t wush_adapter_backward_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax) {
+  if (n < 0 || n > kMaxTokens || d_in < 8 || d_in % 8 || d_out < 8 || d_out % 8 || nseg < 1 || nseg > kMaxSeg || nad < 1 || !rank_ok(rmax))
+    return 0;
+  return round256(part_bytes(n, d_out, nseg, rmax)) + round256(static_cast<size_t>(n) * rmax * sizeof(float)) +
+         adapter_grads_ws_bytes(n, d_in, d_out, nseg, nad, rmax);
+}
+
+extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wush_dtype ydt, int n, int d_in, int d_out,
+                                             const void* dY, int64_t ldg, const void* X, const uint8_t* x_scales,
+                                             int64_t ldx, int nseg, const int* seg_off, const int* seg_adapter,
+                                             int nad, int rmax, const void* A, const void* Bt, const int* rank,
+                                             const float* alpha, const float* V, const void* dX0, int64_t lddx0,
+                                             void* dX, int64_t lddx, float* dA, float* dBt, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  const char* who = "wush_adapter_backward";
+  const wush_status st = check(who, gdt, xdt, ydt, n, d_in, d_out, nseg, nad, rmax);
+  if (st != WUSH_OK) return st;
+  if (ldg < d_out || ldg % 8 || ldx < d_in || ldx % 8 || (dX && (lddx < d_in || lddx % 8)) ||
+      (dX && dX0 && (lddx0 < d_in || lddx0 % 8)))
+    return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
+  if (!adapter_grads_fit(n, d_in, d_out, nad)) return fail(WUSH_E_SHAPE, "%s: nad=%d passes the launch limit", who, nad);
+  if (x_scales && (d_in % 32 || ldx != d_in))
+    return fail(WUSH_E_SHAPE, "%s: an act8 checkpoint has whole groups of 32 and no row stride of its own", who);
+  if (!seg_off || !seg_adapter || !A || !Bt || !rank || !alpha || !dA || !dBt || (n > 0 && (!dY || !X || !V)))
+    return fail(WUSH_E_ARG, "%s: null pointer", who);
+  for (const void* p : {dY, X, A, Bt, static_cast<const void*>(V), dX0, static_cast<const void*>(dX),
+                        static_cast<const void*>(dA), static_cast<const void*>(dBt), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  const size_t need = wush_adapter_backward_ws_bytes(n, d_in, d_out, nseg, nad, rmax);
+  if (ws && ws_bytes < need) return fail(WUSH_E_ARG, "%s: workspace of %zu bytes, need %zu", who, ws_bytes, need);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  void* base = ws;
+  if (!ws) {
+    const hipError_t e = hipMallocAsync(&base, need, s);
+    if (e != hipSuccess) return fail(WUSH_E_HIP, "%s: scratch: %s", who, hipGetErrorString(e));
+  }
+  float* part = static_cast<float*>(base);
+  float* dV = reinterpret_cast<float*>(static_cast<char*>(base) + round256(part_bytes(n, d_out, nseg, rmax)));
+  char* rest = reinterpret_cast<char*>(dV) + round256(static_cast<size_t>(n) * rmax * sizeof(float));
+  wush_status out = WUSH_OK;
+  if (n > 0) {
+    const int splits = low_splits(n, d_out, nseg, rmax);
+    auto f = gdt == WUSH_F32 ? low<float> : low<bf16_t>;
+    f(n, d_out, dY, ldg, nseg, seg_off, seg_adapter, nad, rmax, Bt, rank, alpha, part, s);
+    out = launched(who);
+    if (out == WUSH_OK && dX) {
+      auto g = ydt == WUSH_F32 ? spread<float> : spread<bf16_t>;
+      g(n, d_in, part, splits, nseg, seg_off, seg_adapter, nad, rmax, A, rank, dX0, lddx0, dX, lddx, dV, s);
+      out = launched(who);
+    } else if (out == WUSH_OK) {
+      const int64_t count = static_cast<int64_t>(n) * rmax;
+      hipLaunchKernelGGL(adapter_sum_kernel, dim3(static_cast<unsigned>((count + 255) / 256)), dim3(256), 0, s, count,
+                         part, splits, dV);
+      out = launched(who);
+    }
+  }
+  if (out == WUSH_OK)
+    out = adapter_grads(who, gdt, x_scales ? kAct8 : static_cast<int>(xdt), n, d_in, d_out, dY, ldg, X, x_scales, ldx,
+                        nseg, seg_off, seg_adapter, nad, rmax, rank, V, dV, dA, dBt, rest, s);
+  if (!ws) (void)hipFreeAsync(base, s);
+  return out;
+}

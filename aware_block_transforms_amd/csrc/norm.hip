@@ -1,0 +1,484 @@
+// Block norm: what stands between two blocks of a model, in one pass.
+//
+// Per token, with y the block's output and r the residual stream:
+//   b  = y rsqrt(mean(y^2) + eps) * w_post * gate      (norm after the block)
+//   r' = res r + branch b                              (gate and residual scale)
+//   u  = r' rsqrt(mean(r'^2) + eps) * w_pre            (norm before the next)
+// The gate is absent, one value per channel, per token or per element.  u is
+// computed from r' before r' is rounded to its storage type.
+//
+// Backward, with k1, k2 the two rsqrt values kept by the forward call, and y
+// and r' as stored:
+//   x  = k2 r',  q = dU w_pre,   t = dR' + k2 (q - x mean(q x)),   dw_pre = sum dU x
+//   z  = k1 y,   g = branch t,   dgate = g z w_post,               dw_post = sum g gate z
+//   p  = g gate w_post,          dY = k1 (p - z mean(p z)),        dR = res t
+// All sums are fp32.
+//
+// Both directions are bound by HBM: every value is read and written once.  A
+// workgroup owns a row, a thread VPT pieces of eight values of it, which stay
+// in registers between the two means.  In the backward kernel a workgroup
+// walks over rows and keeps its columns' weight gradients in registers; the
+// workgroups' sums are written once and added in a fixed order by a second
+// kernel, so results do not depend on scheduling.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "common.h"
+#include "vec.h"
+
+using namespace wush;
+
+namespace {
+
+// Sum of each of N values over the workgroup, in every thread; `slot` holds 16
+// floats per value and is not reused before the next barrier but one.
+template <int N>
+__device__ __forceinline__ void block_sums(float* v, float* slot) {
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) slot[i * 16 + wave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = 0.0f;
+    for (int w = 0; w < waves; ++w) s += slot[i * 16 + w];
+    v[i] = s;
+  }
+}
+
+__device__ __forceinline__ void load_weights(const float* w, int col, float* v) {
+  raw8<float> r;
+  load8(r, w + col);
+  widen8(r, v);
+}
+
+struct NormArgs {
+  int n, d;
+  const float* w_post;
+  const float* w_pre;
+  const void* gate;
+  float branch, res, eps;
+  float* k1;
+  float* k2;
+};
+
+template <class Y, class R, class U, int VPT>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kind, const Y* __restrict__ y,
+                                                        const R* r, R* rout, U* __restrict__ u) {
+  __shared__ float slots[2][16];
+  const int64_t row = blockIdx.x, base = row * a.d;
+  raw8<Y> ry[VPT];
+  raw8<R> rr[VPT];
+  raw8<Y> rg[VPT];
+  int col[VPT];
+  bool in[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    col[v] = (v * blockDim.x + threadIdx.x) * 8;
+    in[v] = col[v] < a.d;
+    if (in[v]) {
+      if (y) load8(ry[v], y + base + col[v]);
+      load8(rr[v], r + base + col[v]);
+      if (gate_kind == WUSH_GATE_ELEMENT) load8(rg[v], static_cast<const Y*>(a.gate) + base + col[v]);
+    }
+  }
+  float x[VPT][8];
+  float k1 = 1.0f;
+  if (y) {
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!in[v]) continue;
+      widen8(ry[v], x[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[v][i], x[v][i], s);
+    }
+    if (a.w_post) {
+      block_sums<1>(&s, slots[0]);
+      k1 = 1.0f / __builtin_sqrtf(s / a.d + a.eps);
+      if (a.k1 && threadIdx.x == 0) a.k1[row] = k1;
+    }
+  }
+  float scale = a.branch * k1;
+  if (gate_kind == WUSH_GATE_TOKEN) scale *= static_cast<const float*>(a.gate)[row];
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (!in[v]) continue;
+    float t[8];
+    widen8(rr[v], t);
+    if (y) {
+      float w[8];
+      if (a.w_post) {
+        load_weights(a.w_post, col[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v][i] *= w[i];
+      }
+      if (gate_kind == WUSH_GATE_CHANNEL) {
+        load_weights(static_cast<const float*>(a.gate), col[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v][i] *= w[i];
+      } else if (gate_kind == WUSH_GATE_ELEMENT) {
+        widen8(rg[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v][i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[v][i] = __builtin_fmaf(x[v][i], scale, a.res * t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[v][i] = a.res * t[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[v][i], x[v][i], s);
+    if (rout) store8(rout + base + col[v], x[v]);
+  }
+  if (!a.w_pre) return;
+  block_sums<1>(&s, slots[1]);
+  const float k2 = 1.0f / __builtin_sqrtf(s / a.d + a.eps);
+  if (a.k2 && threadIdx.x == 0) a.k2[row] = k2;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (!in[v]) continue;
+    float w[8];
+    load_weights(a.w_pre, col[v], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= x[v][i] * k2;
+    store8(u + base + col[v], w);
+  }
+}
+
+// Partial column sums of one workgroup: [3][d] (dw_pre, dw_post, dgate).  A row
+// stays in registers as it lies in memory and is widened where it is used, so
+// that the columns' sums fit beside it.  MAXT: the largest workgroup, which
+// sets the registers a thread may have.
+template <class Y, class R, class U, int VPT, int MAXT, bool CHANNEL>
+__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kind, const U* __restrict__ du,
+                                                        const R* drout, const Y* __restrict__ y,
+                                                        const R* __restrict__ rout, Y* __restrict__ dy, R* dr,
+                                                        void* __restrict__ dgate, float* __restrict__ part) {
+  __shared__ float slots[2][2 * 16];
+  int col[VPT];
+  bool in[VPT];
+  float s_pre[VPT][8], s_post[VPT][8], s_gate[CHANNEL ? VPT : 1][8];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    col[v] = (v * blockDim.x + threadIdx.x) * 8;
+    in[v] = col[v] < a.d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s_pre[v][i] = s_post[v][i] = 0.0f;
+      if (CHANNEL) s_gate[v][i] = 0.0f;
+    }
+  }
+  const float inv_d = 1.0f / a.d;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const int64_t base = row * a.d;
+    raw8<Y> ry[VPT], rg[VPT];
+    raw8<R> rr[VPT], rd[VPT];
+    raw8<U> ru[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!in[v]) continue;
+      if (a.w_pre) {
+        load8(ru[v], du + base + col[v]);
+        load8(rr[v], rout + base + col[v]);
+      }
+      if (drout) load8(rd[v], drout + base + col[v]);
+      if (y) load8(ry[v], y + base + col[v]);
+      if (gate_kind == WUSH_GATE_ELEMENT) load8(rg[v], static_cast<const Y*>(a.gate) + base + col[v]);
+    }
+    const float k1 = y && a.w_post ? a.k1[row] : 1.0f;
+    const float k2 = a.w_pre ? a.k2[row] : 0.0f;
+    float m = 0.0f;
+    if (a.w_pre) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if (!in[v]) continue;
+        float w[8], q[8], x[8];
+        widen8(ru[v], q);
+        widen8(rr[v], x);
+        load_weights(a.w_pre, col[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float qx = q[i] * (x[i] * k2);
+          s_pre[v][i] += qx;
+          m = __builtin_fmaf(qx, w[i], m);
+        }
+      }
+      block_sums<1>(&m, slots[0]);
+      m *= inv_d;
+    }
+    float sums[2] = {0.0f, 0.0f};   // p z, and the token gate's gradient
+    float p[VPT][8];
+    const float gate_t = gate_kind == WUSH_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!in[v]) continue;
+      float t[8], w[8], o[8];
+      if (drout) {
+        widen8(rd[v], t);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = 0.0f;
+      }
+      if (a.w_pre) {
+        float q[8], x[8];
+        widen8(ru[v], q);
+        widen8(rr[v], x);
+        load_weights(a.w_pre, col[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __builtin_fmaf(k2, __builtin_fmaf(-x[i] * k2, m, q[i] * w[i]), t[i]);
+      }
+      if (dr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = a.res * t[i];
+        store8(dr + base + col[v], o);
+      }
+      if (!y) continue;
+      float z[8], g[8];
+      widen8(ry[v], z);
+      if (a.w_post) {
+        load_weights(a.w_post, col[v], w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+      }
+      if (CHANNEL) {
+        load_weights(static_cast<const float*>(a.gate), col[v], g);
+      } else if (gate_kind == WUSH_GATE_ELEMENT) {
+        widen8(rg[v], g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = gate_t;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = a.branch * t[i];
+        z[i] *= k1;
+        const float hz = h * z[i], dg = hz * w[i];
+        o[i] = dg;
+        if (CHANNEL) s_gate[v][i] += dg;
+        sums[1] += dg;
+        s_post[v][i] = __builtin_fmaf(hz, g[i], s_post[v][i]);
+        p[v][i] = h * g[i] * w[i];
+        sums[0] = __builtin_fmaf(p[v][i], z[i], sums[0]);
+      }
+      if (gate_kind == WUSH_GATE_ELEMENT) store8(static_cast<Y*>(dgate) + base + col[v], o);
+    }
+    if (!y) {
+      if (a.w_pre) __syncthreads();   // slots[0] is read before the next row writes it
+      continue;
+    }
+    block_sums<2>(sums, slots[1]);
+    if (gate_kind == WUSH_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(dgate)[row] = sums[1];
+    // without a norm after the block dY is p itself
+    const float mz = a.w_post ? k1 * sums[0] * inv_d : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!in[v]) continue;
+      float z[8];
+      widen8(ry[v], z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[v][i] = k1 * __builtin_fmaf(-z[i], mz, p[v][i]);
+      store8(dy + base + col[v], p[v]);
+    }
+    if (!a.w_pre) __syncthreads();   // slots[1] likewise, where one barrier a row is all there is
+  }
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 3 * a.d;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (!in[v]) continue;
+    if (a.w_pre) store8(out + col[v], s_pre[v]);
+    if (y && a.w_post) store8(out + a.d + col[v], s_post[v]);
+    if (CHANNEL) store8(out + 2 * a.d + col[v], s_gate[v]);
+  }
+}
+
+// Adds the workgroups' column sums: 64 columns a workgroup, its 16 waves take
+// every 16th partial and are joined in order.
+__global__ __launch_bounds__(1024) void norm_cols_kernel(int d, int parts, const float* __restrict__ part,
+                                                         float* __restrict__ dw_pre, float* __restrict__ dw_post,
+                                                         float* __restrict__ dgate) {
+  __shared__ float sh[16][64];
+  float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (c < d)
+    for (int i = wave; i < parts; i += 16) s += part[(static_cast<int64_t>(i) * 3 + blockIdx.y) * d + c];
+  sh[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= d) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += sh[w][lane];
+  out[c] = s;
+}
+
+constexpr int kMaxD = 24576;
+
+// Pieces of eight values per thread of the forward kernel: two, whose loads are
+// in flight together, up to the largest workgroup's 16384 columns.
+int fwd_vpt(int d) { return d <= 16384 ? 2 : 4; }
+
+// The backward kernel's: two up to 8192 columns.  Wider rows take more per
+// thread, so that a workgroup of eight waves (twelve past 16384 columns) still
+// leaves each thread 256 (168) registers for the columns' sums.
+int bwd_vpt(int d) { return d <= 8192 ? 2 : d <= 12288 ? 3 : 4; }
+
+int threads(int d, int vpt) {
+  const int per = 8 * vpt * 64;
+  return 64 * ((d + per - 1) / per);
+}
+
+// Workgroups of the backward kernel: about twelve waves for each of the 256
+// compute units, which is what fits, but each with eight rows at least while
+// every unit has one.
+int bwd_groups(int n, int d) {
+  const int waves = threads(d, bwd_vpt(d)) / 64;
+  const int fit = 256 * ((12 + waves - 1) / waves), rows = (n + 7) / 8;
+  const int g = rows < fit ? rows : fit;
+  return g >= 256 ? g : n < 256 ? n : 256;
+}
+
+wush_status check(const char* who, wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d, wush_gate gate_kind,
+                  const void* Y, const void* gate, const float* w_post, const float* w_pre, float branch, float res) {
+  for (wush_dtype t : {ydt, rdt, udt})
+    if (t != WUSH_F32 && t != WUSH_BF16) return fail(WUSH_E_ARG, "%s: bad dtype", who);
+  if (rdt == WUSH_BF16 && udt == WUSH_F32)
+    return fail(WUSH_E_UNSUPPORTED, "%s: an fp32 norm output beside a bf16 residual", who);
+  if (n < 0 || d < 8 || d % 8 || d > kMaxD)
+    return fail(WUSH_E_SHAPE, "%s: need n >= 0 and d a multiple of 8 in 8..%d (n=%d d=%d)", who, kMaxD, n, d);
+  if (gate_kind < WUSH_GATE_NONE || gate_kind > WUSH_GATE_ELEMENT) return fail(WUSH_E_ARG, "%s: bad gate kind", who);
+  if (n == 0) return WUSH_OK;   // an empty tensor may have no address
+  if ((gate_kind != WUSH_GATE_NONE) != (gate != nullptr)) return fail(WUSH_E_ARG, "%s: a gate needs its kind and its pointer", who);
+  if (!Y && (gate || w_post)) return fail(WUSH_E_ARG, "%s: w_post and the gate need Y", who);
+  if (!Y && !w_pre) return fail(WUSH_E_ARG, "%s: nothing to do without Y and w_pre", who);
+  if (!__builtin_isfinite(branch) || !__builtin_isfinite(res)) return fail(WUSH_E_ARG, "%s: scales must be finite", who);
+  return WUSH_OK;
+}
+
+template <class F>
+wush_status by_types(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, F f) {
+  const bool y = ydt == WUSH_F32, r = rdt == WUSH_F32, u = udt == WUSH_F32;
+  if (y) {
+    if (r) return u ? f(float(), float(), float()) : f(float(), float(), bf16_t());
+    return f(float(), bf16_t(), bf16_t());
+  }
+  if (r) return u ? f(bf16_t(), float(), float()) : f(bf16_t(), float(), bf16_t());
+  return f(bf16_t(), bf16_t(), bf16_t());
+}
+
+wush_status launched(const char* who) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? WUSH_OK : fail(WUSH_E_HIP, "%s launch: %s", who, hipGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d, const void* Y,
+                                       const float* w_post, wush_gate gate_kind, const void* gate, float branch_scale,
+                                       const void* R, float res_scale, const float* w_pre, float eps, void* Rout,
+                                       void* U, float* rstd_post, float* rstd_pre, void* stream) {
+  const char* who = "wush_block_norm";
+  const wush_status st =
+      check(who, ydt, rdt, udt, n, d, gate_kind, Y, gate, w_post, w_pre, branch_scale, res_scale);
+  if (st != WUSH_OK) return st;
+  if (!(eps > 0.0f) || !__builtin_isfinite(eps)) return fail(WUSH_E_ARG, "%s: eps must be positive and finite", who);
+  if (n == 0) return WUSH_OK;
+  if ((w_pre != nullptr) != (U != nullptr)) return fail(WUSH_E_ARG, "%s: w_pre and U are given together", who);
+  if (!R || (!U && !Rout)) return fail(WUSH_E_ARG, "%s: null pointer", who);
+  for (const void* p : {Y, static_cast<const void*>(w_post), R, static_cast<const void*>(w_pre),
+                        static_cast<const void*>(Rout), static_cast<const void*>(U)})
+    if (!aligned16(p)) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  if (!aligned16(gate) && gate_kind != WUSH_GATE_TOKEN) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  const NormArgs a{n, d, w_post, w_pre, gate, branch_scale, res_scale, eps, rstd_post, rstd_pre};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return by_types(ydt, rdt, udt, [&](auto y, auto r, auto u) {
+    using YT = decltype(y);
+    using RT = decltype(r);
+    using UT = decltype(u);
+    auto k = fwd_vpt(d) == 2 ? norm_fwd_kernel<YT, RT, UT, 2> : norm_fwd_kernel<YT, RT, UT, 4>;
+    hipLaunchKernelGGL(k, dim3(n), dim3(threads(d, fwd_vpt(d))), 0, s, a, static_cast<int>(gate_kind), static_cast<const YT*>(Y),
+                       static_cast<const RT*>(R), static_cast<RT*>(Rout), static_cast<UT*>(U));
+    return launched(who);
+  });
+}
+
+extern "C" size_t wush_block_norm_bwd_ws_bytes(int n, int d) {
+  if (n < 1 || d < 8 || d % 8 || d > kMaxD) return 0;
+  return static_cast<size_t>(bwd_groups(n, d)) * 3 * d * sizeof(float);
+}
+
+extern "C" wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d,
+                                           const void* dU, const void* dRout, const void* Y, const float* w_post,
+                                           wush_gate gate_kind, const void* gate, float branch_scale, const void* Rout,
+                                           float res_scale, const float* w_pre, const float* rstd_post,
+                                           const float* rstd_pre, void* dY, void* dR, void* dgate, float* dw_post,
+                                           float* dw_pre, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "wush_block_norm_bwd";
+  const wush_status st =
+      check(who, ydt, rdt, udt, n, d, gate_kind, Y, gate, w_post, w_pre, branch_scale, res_scale);
+  if (st != WUSH_OK) return st;
+  if (n > 0) {
+    if ((w_pre != nullptr) != (dU != nullptr) || (w_pre != nullptr) != (dw_pre != nullptr))
+      return fail(WUSH_E_ARG, "%s: w_pre, dU and dw_pre are given together", who);
+    if ((w_post != nullptr) != (dw_post != nullptr)) return fail(WUSH_E_ARG, "%s: w_post and dw_post are given together", who);
+    if ((Y != nullptr) != (dY != nullptr)) return fail(WUSH_E_ARG, "%s: Y and dY are given together", who);
+    if ((gate != nullptr) != (dgate != nullptr)) return fail(WUSH_E_ARG, "%s: gate and dgate are given together", who);
+    if (!dU && !dRout) return fail(WUSH_E_ARG, "%s: no gradient given", who);
+    if ((w_pre && (!Rout || !rstd_pre)) || (w_post && !rstd_post)) return fail(WUSH_E_ARG, "%s: null pointer", who);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  for (const void* p : {dU, dRout, Y, static_cast<const void*>(w_post), Rout, static_cast<const void*>(w_pre),
+                        static_cast<const void*>(dY), static_cast<const void*>(dR), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  if ((!aligned16(gate) || !aligned16(dgate)) && gate_kind != WUSH_GATE_TOKEN)
+    return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
+  float* gate_cols = gate_kind == WUSH_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
+  const bool cols = dw_pre || dw_post || gate_cols;
+  const size_t need = cols ? wush_block_norm_bwd_ws_bytes(n, d) : 0;
+  if (ws && ws_bytes < need) return fail(WUSH_E_ARG, "%s: workspace of %zu bytes, need %zu", who, ws_bytes, need);
+  float* part = static_cast<float*>(ws);
+  if (need && !ws) {
+    const hipError_t e = hipMallocAsync(reinterpret_cast<void**>(&part), need, s);
+    if (e != hipSuccess) return fail(WUSH_E_HIP, "%s: scratch: %s", who, hipGetErrorString(e));
+  }
+  const NormArgs a{n, d, w_post, w_pre, gate, branch_scale, res_scale, 0.0f, const_cast<float*>(rstd_post),
+                   const_cast<float*>(rstd_pre)};
+  const int groups = n > 0 ? bwd_groups(n, d) : 0;
+  wush_status out = WUSH_OK;
+  if (n > 0)
+    out = by_types(ydt, rdt, udt, [&](auto y, auto r, auto u) {
+      using YT = decltype(y);
+      using RT = decltype(r);
+      using UT = decltype(u);
+      auto pick = [&](auto channel) {
+        constexpr bool C = decltype(channel)::value;
+        return d <= 8192    ? norm_bwd_kernel<YT, RT, UT, 2, 512, C>
+               : d <= 12288 ? norm_bwd_kernel<YT, RT, UT, 3, 512, C>
+               : d <= 16384 ? norm_bwd_kernel<YT, RT, UT, 4, 512, C>
+                            : norm_bwd_kernel<YT, RT, UT, 4, 768, C>;
+      };
+      auto k = gate_kind == WUSH_GATE_CHANNEL ? pick(std::true_type()) : pick(std::false_type());
+      hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a, static_cast<int>(gate_kind),
+                         static_cast<const UT*>(dU), static_cast<const RT*>(dRout), static_cast<const YT*>(Y),
+                         static_cast<const RT*>(Rout), static_cast<YT*>(dY), static_cast<RT*>(dR), dgate, part);
+      return launched(who);
+    });
+  if (out == WUSH_OK && cols) {
+    hipLaunchKernelGGL(norm_cols_kernel, dim3((d + 63) / 64, 3), dim3(1024), 0, s, d, groups, part, dw_pre, dw_post,
+                       gate_cols);
+    out = launched(who);
+  }
+  if (need && !ws) (void)hipFreeAsync(part, s);
+  return out;
+}

@@ -398,6 +398,152 @@ wush_status wush_had256_gemv(int batch, int d_out, int d_in, const uint16_t* x,
  *   in, out  device, [rows][d_in] fp32, d_in % 256 == 0. */
 wush_status wush_had256_rotate(int rows, int d_in, const float* in, float* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around a frozen projection: the norm between blocks, activations kept in 8
+ * bits for the backward pass, and low-rank adapters beside the projection.
+ * Row pointers are 16-byte aligned and row lengths multiples of 8; tensors
+ * typed wush_dtype are fp32 or bf16, and bf16 outputs are rounded once, to
+ * nearest even, from fp32 values.  No call uses atomics on floats: the same
+ * inputs give the same bits.
+ * ---------------------------------------------------------------------- */
+
+/* What multiplies a block's normed output: nothing, fp32 [d], fp32 [n], or
+ * [n][d] in Y's type. */
+typedef enum {
+  WUSH_GATE_NONE = 0,
+  WUSH_GATE_CHANNEL = 1,
+  WUSH_GATE_TOKEN = 2,
+  WUSH_GATE_ELEMENT = 3
+} wush_gate;
+
+/* Norm after a block, gate, residual scale, residual sum and the norm before
+ * the next block, per token:
+ *   b  = Y rsqrt(mean(Y^2) + eps) w_post gate
+ *   R' = res_scale R + branch_scale b
+ *   U  = R' rsqrt(mean(R'^2) + eps) w_pre
+ * Means over the row's d values; fp32 arithmetic throughout, U from R' before
+ * R' is rounded to its type.
+ *   Y       device, [n][d] (ydt), for instance the matmul's output, or NULL: R'
+ *           = res_scale R (the norm before a model's first block).
+ *   w_post  device, fp32 [d], or NULL: no norm after the block, b = Y gate.
+ *   gate    device, as gate_kind says; NULL for WUSH_GATE_NONE.
+ *   R       device, [n][d] (rdt).          Rout  device out, likewise; may be R, or
+ *           NULL if only U is wanted.
+ *   w_pre   device, fp32 [d], or NULL together with U: no norm after the sum.
+ *   U       device out, [n][d] (udt; not fp32 beside a bf16 R), for instance
+ *           the input of wush_transform_quant.
+ *   rstd_post, rstd_pre  device out, fp32 [n]: the two rsqrt values, which the
+ *           backward call needs; or NULL.
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0; d not a multiple of 8 in 8..24576),
+ * WUSH_E_UNSUPPORTED (udt), WUSH_E_HIP. */
+wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d,
+                            const void* Y, const float* w_post, wush_gate gate_kind,
+                            const void* gate, float branch_scale, const void* R, float res_scale,
+                            const float* w_pre, float eps, void* Rout, void* U, float* rstd_post,
+                            float* rstd_pre, void* stream);
+
+/* Its gradients, from dU and dRout (either may be NULL, not both; dU goes with
+ * w_pre) and the forward call's Y, Rout and rstd values.
+ *   dY      device out, [n][d] (ydt), with Y.   dR  device out, [n][d] (rdt), or NULL;
+ *           may be dRout.
+ *   dgate   device out, the gate's shape and type, with gate.
+ *   dw_post, dw_pre  device out, fp32 [d], with w_post and w_pre.
+ *   ws      device scratch of wush_block_norm_bwd_ws_bytes(n, d) bytes, or
+ *           NULL (taken from the default memory pool for the call).
+ * n = 0 clears the sums over tokens.  Errors: as above. */
+size_t wush_block_norm_bwd_ws_bytes(int n, int d);
+wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d,
+                                const void* dU, const void* dRout, const void* Y,
+                                const float* w_post, wush_gate gate_kind, const void* gate,
+                                float branch_scale, const void* Rout, float res_scale,
+                                const float* w_pre, const float* rstd_post, const float* rstd_pre,
+                                void* dY, void* dR, void* dgate, float* dw_post, float* dw_pre,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* act8: a checkpoint of activations in 8.25 bits.  Every 32 values of a row
+ * (d % 32 == 0) share one scale byte:
+ *   a = max|x|, e = clamp(floor(log2 a), -120, 127) (a = 0: -120), byte e + 127,
+ *   q = clamp(rint(x 2^(6-e)), -127, 127), which stands for q 2^(e-6).
+ * The error is at most 2^(e-7), 2^(e-6) for values from 127.5 2^(e-6) on.
+ * A group with a NaN or an infinity gets byte 0xFF and zero codes, and stands
+ * for NaN.  Every value is a bf16 number.
+ *   codes   device, [n][d] int8, 16-byte aligned.   scales  device, [n][d/32] bytes.
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0, d % 32), WUSH_E_HIP. */
+wush_status wush_act8_pack(wush_dtype xdt, int n, int d, const void* X, int8_t* codes,
+                           uint8_t* scales, void* stream);
+wush_status wush_act8_unpack(wush_dtype ydt, int n, int d, const int8_t* codes,
+                             const uint8_t* scales, void* Y, void* stream);
+
+/* The gated activation of an MLP, H = G sigmoid(G) U, which also keeps G and U
+ * as act8 checkpoints (the four checkpoint pointers together, or NULL when no
+ * backward pass follows).  G and U are [n][d] (xdt) with a row stride of ld
+ * values, such as the halves of one projection's output; H is [n][d] (hdt). */
+wush_status wush_act8_swiglu(wush_dtype xdt, wush_dtype hdt, int n, int d, const void* G,
+                             const void* U, int64_t ld, void* H, int8_t* g_codes,
+                             uint8_t* g_scales, int8_t* u_codes, uint8_t* u_scales, void* stream);
+
+/* Its gradient at the checkpoints' values g and u, with s = sigmoid(g):
+ *   dU = dH g s,   dG = dH u s (1 + g (1 - s)).
+ * dH is [n][d] (hdt), dG and dU [n][d] (xdt) with a row stride of ld values. */
+wush_status wush_act8_swiglu_bwd(wush_dtype hdt, wush_dtype xdt, int n, int d, const void* dH,
+                                 const int8_t* g_codes, const uint8_t* g_scales,
+                                 const int8_t* u_codes, const uint8_t* u_scales, void* dG, void* dU,
+                                 int64_t ld, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection.  The n tokens
+ * are runs of nseg requests: request s owns the tokens [seg_off[s],
+ * seg_off[s+1]), with seg_off[0] = 0 and seg_off[nseg] = n (rising; a request
+ * may be empty), and uses adapter seg_adapter[s], or none if that lies outside
+ * [0, nad).  Of adapter a's rows the first rank[a] count (0..rmax; the others
+ * are not used), and its factor is alpha[a].  For its tokens
+ *   V = alpha X A^T,   Y = Y0 + V Bt;
+ * the others get Y = Y0 and V = 0.
+ *   X     device, [n][d_in] (xdt), row stride ldx.
+ *   seg_off, seg_adapter  device int32, [nseg + 1] and [nseg].
+ *   A     device bf16, [nad][rmax][d_in]; Bt device bf16, [nad][rmax][d_out], the
+ *         transpose of the factor that is usually called B.  rmax is 16, 32, 64
+ *         or 128.       rank  device int32 [nad].       alpha  device fp32 [nad].
+ *   Y0    device, [n][d_out] (ydt), row stride ldy0, for instance the
+ *         projection's output, or NULL for zeros.
+ *   Y     device out, [n][d_out] (ydt), row stride ldy; may be Y0.
+ *   V     device out, fp32 [n][rmax], which the backward call needs, or NULL.
+ *   ws    device scratch of wush_adapter_ws_bytes(n, d_in, nseg, rmax) bytes, or
+ *         NULL (taken from the default memory pool for the call).
+ * V is held and used as fp32 (split into exact bf16 terms for the matrix
+ * cores), and sums are fp32.  An infinity in V makes its results NaN.
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (sizes, strides, rmax), WUSH_E_HIP. */
+size_t wush_adapter_ws_bytes(int n, int d_in, int nseg, int rmax);
+wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int n, int d_in, int d_out,
+                                 const void* X, int64_t ldx, int nseg, const int* seg_off,
+                                 const int* seg_adapter, int nad, int rmax, const void* A,
+                                 const void* Bt, const int* rank, const float* alpha,
+                                 const void* Y0, int64_t ldy0, void* Y, int64_t ldy, float* V,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients of the adapters and of their input, from dY and the forward
+ * call's V:
+ *   dV = alpha dY Bt^T,  dX = dX0 + dV A,  dA = dV^T X,  dBt = V^T dY,
+ * dA and dBt summed over all tokens of an adapter, zero in rows that do not
+ * count and for adapters without tokens.
+ *   dY    device, [n][d_out] (gdt), row stride ldg.
+ *   X     device, [n][d_in] (xdt), row stride ldx; or, with x_scales, the codes of
+ *         an act8 checkpoint of it (ldx = d_in, xdt unused).
+ *   dX0   device, [n][d_in] (ydt), row stride lddx0, the projection's own input
+ *         gradient, or NULL for zeros.  dX  device out, likewise (lddx); may be
+ *         dX0, or NULL if not wanted.
+ *   dA, dBt  device out, fp32, shaped like A and Bt.
+ *   ws    device scratch of wush_adapter_backward_ws_bytes(...) bytes, or NULL.
+ * Errors: as above. */
+size_t wush_adapter_backward_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax);
+wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wush_dtype ydt, int n, int d_in,
+                                  int d_out, const void* dY, int64_t ldg, const void* X,
+                                  const uint8_t* x_scales, int64_t ldx, int nseg,
+                                  const int* seg_off, const int* seg_adapter, int nad, int rmax,
+                                  const void* A, const void* Bt, const int* rank,
+                                  const float* alpha, const float* V, const void* dX0,
+                                  int64_t lddx0, void* dX, int64_t lddx, float* dA, float* dBt,
+                                  void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------ */
 const char* wush_status_string(wush_status s);
 const char* wush_last_error(void);
