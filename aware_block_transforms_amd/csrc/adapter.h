@@ -62,25 +62,39 @@ __device__ __forceinline__ int request_start(const int* __restrict__ off, int s,
 template <int T>
 __device__ __forceinline__ Tile find_tile(int number, int n, int nseg, const int* __restrict__ off,
                                           const int* __restrict__ ids, int nad) {
-  // every wave counts the requests whose first tile is not past `number`
+  // every wave counts the requests whose first tile is not past `number`; the
+  // count's last request is the tile's.  Of up to 64 requests the lanes hold
+  // everything needed, one load after another is saved.
   const int lane = threadIdx.x & 63;
-  int count = 0;
-  for (int b = 0; b < nseg; b += 64) {
-    const int s = b + lane;
-    const bool le = s < nseg && request_start(off, s, nseg, n) / T + s <= number;
-    count += __popcll(__ballot(le));
-  }
   Tile t{0, 0, -1};
-  const int s = __builtin_amdgcn_readfirstlane(count - 1);
-  if (s < 0) return t;
-  const int first = request_start(off, s, nseg, n), last = request_start(off, s + 1, nseg, n);
+  int s, first, last, a;
+  if (nseg <= 64) {
+    const int start = request_start(off, lane, nseg, n);
+    const int id = lane < nseg ? ids[lane] : -1;
+    s = __popcll(__ballot(lane < nseg && start / T + lane <= number)) - 1;
+    if (s < 0) return t;
+    s = __builtin_amdgcn_readfirstlane(s);
+    first = __builtin_amdgcn_readlane(start, s);
+    last = s + 1 < nseg ? __builtin_amdgcn_readlane(start, s + 1) : n;
+    a = __builtin_amdgcn_readlane(id, s);
+  } else {
+    int count = 0;
+    for (int b = 0; b < nseg; b += 64) {
+      const int q = b + lane;
+      count += __popcll(__ballot(q < nseg && request_start(off, q, nseg, n) / T + q <= number));
+    }
+    s = __builtin_amdgcn_readfirstlane(count - 1);
+    if (s < 0) return t;
+    first = request_start(off, s, nseg, n);
+    last = request_start(off, s + 1, nseg, n);
+    a = ids[s];
+  }
   const int j = number - (first / T + s);
   // 64 bits: j runs far past the request's end on unused numbers
   const int64_t begin = first + static_cast<int64_t>(j) * T;
   if (j < 0 || begin >= last) return t;
   t.begin = static_cast<int>(begin);
   t.end = last - t.begin < T ? last : t.begin + T;
-  const int a = ids[s];
   t.adapter = a >= 0 && a < nad ? a : -1;
   return t;
 }

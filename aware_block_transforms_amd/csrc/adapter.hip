@@ -30,7 +30,7 @@ wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int
                           int64_t ldg, const void* X, const uint8_t* x_scales, int64_t ldx, int nseg,
                           const int* seg_off, const int* seg_adapter, int nad, int rmax, const int* rank,
                           const float* V, const float* dV, float* dA, float* dBt, void* ws, hipStream_t s);
-bool adapter_grads_fit(int n, int d_in, int d_out, int nad);
+bool adapter_grads_fit(int n, int d_in, int d_out, int nad, int rmax);
 size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax);
 }  // namespace wush
 
@@ -88,6 +88,50 @@ struct XOps<float> {
   }
 };
 
+// The product over a wave's pieces of k, for NT row tiles of the factor.
+template <class X, int NT, int RT, int TT>
+__device__ __forceinline__ void low_pieces(const X* const (&xp)[TT], const bf16_t* const (&fp)[RT], int k, int d,
+                                           int step, f32x4 (&acc)[TT][RT]) {
+  struct Piece {
+    XOps<X> x[TT];
+    XOps<bf16_t> f[NT];
+  };
+  const int g = (threadIdx.x & 63) >> 4;
+  auto load = [&](Piece& p, int at) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) p.x[i].load(xp[i] + at);
+#pragma unroll
+    for (int r = 0; r < NT; ++r) p.f[r].load(fp[r] + at);
+  };
+  auto multiply = [&](const Piece& p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        u32x4 xt[3];
+        p.x[i].operand(h, xt);
+#pragma unroll
+        for (int m = 0; m < XOps<X>::kTerms; ++m)
+#pragma unroll
+          for (int r = 0; r < NT; ++r) acc[i][r] = mfma(xt[m], p.f[r].v[h], acc[i][r]);
+      }
+  };
+  for (; k + 64 <= d; k += step) {
+    Piece p;
+    load(p, k);
+    multiply(p);
+  }
+  if (k < d) {
+    Piece p;
+    const int left = d - k - 16 * g;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) p.x[i].load_tail(xp[i] + k, left);
+#pragma unroll
+    for (int r = 0; r < NT; ++r) p.f[r].load_tail(fp[r] + k, left);
+    multiply(p);
+  }
+}
+
 template <class X, int RT, int TT>
 __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, const X* __restrict__ x, int64_t ldx,
                                                                   int nseg, const int* __restrict__ off,
@@ -97,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
                                                                   const float* __restrict__ alpha,
                                                                   float* __restrict__ part) {
   constexpr int R = 16 * RT, T = 16 * TT;
-  __shared__ float red[kWaves][T * R];
+  __shared__ float red[kWaves][16 * R];
   const Tile t = find_tile<T>(blockIdx.x, n, nseg, off, ids, nad);
   if (t.begin >= t.end) return;
   float* out = part + (static_cast<int64_t>(blockIdx.y) * n + t.begin) * R;
@@ -121,59 +165,35 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
   for (int i = 0; i < TT; ++i)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[i][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int tiles = (rk + 15) / 16;   // row tiles in use
-  const int step = 64 * kWaves * gridDim.y;
-  auto multiply = [&](const XOps<X>(&xo)[TT], const XOps<bf16_t>(&fo)[RT]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 xt[TT][3];
-#pragma unroll
-      for (int i = 0; i < TT; ++i) xo[i].operand(h, xt[i]);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (r >= tiles) break;
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-#pragma unroll
-          for (int m = 0; m < XOps<X>::kTerms; ++m) acc[i][r] = mfma(xt[i][m], fo[r].v[h], acc[i][r]);
-      }
-    }
-  };
-  int k = 64 * (kWaves * blockIdx.y + wave);
-  for (; k + 64 <= d; k += step) {
-    XOps<X> xo[TT];
-    XOps<bf16_t> fo[RT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) xo[i].load(xp[i] + k);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      if (r < tiles) fo[r].load(fp[r] + k);
-    multiply(xo, fo);
-  }
-  if (k < d) {
-    XOps<X> xo[TT];
-    XOps<bf16_t> fo[RT];
-    const int left = d - k - 16 * g;
-#pragma unroll
-    for (int i = 0; i < TT; ++i) xo[i].load_tail(xp[i] + k, left);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      if (r < tiles) fo[r].load_tail(fp[r] + k, left);
-    multiply(xo, fo);
-  }
-#pragma unroll
-  for (int i = 0; i < TT; ++i)
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][(16 * i + 4 * g + e) * R + 16 * r + j] = acc[i][r][e];
-  __syncthreads();
+  const int step = 64 * kWaves * gridDim.y, k = 64 * (kWaves * blockIdx.y + wave);
+  // row tiles in use, rounded up to a power of two; the extra ones repeat the
+  // last row and are dropped
+  const int tiles = (rk + 15) / 16;
+  if (RT > 4 && tiles > 4)
+    low_pieces<X, RT, RT, TT>(xp, fp, k, d, step, acc);
+  else if (RT > 2 && tiles > 2)
+    low_pieces<X, (RT > 4 ? 4 : RT), RT, TT>(xp, fp, k, d, step, acc);
+  else if (RT > 1 && tiles > 1)
+    low_pieces<X, (RT > 2 ? 2 : RT), RT, TT>(xp, fp, k, d, step, acc);
+  else
+    low_pieces<X, 1, RT, TT>(xp, fp, k, d, step, acc);
   const float f = alpha[t.adapter];
-  for (int i = threadIdx.x; i < rows * R; i += 64 * kWaves) {
-    float s = red[0][i];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += red[w][i];
-    out[i] = i % R < rk ? f * s : 0.0f;
+  for (int i = 0; i < TT; ++i) {
+    if (16 * i >= rows) break;
+    if (i > 0) __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][(4 * g + e) * R + 16 * r + j] = acc[i][r][e];
+    __syncthreads();
+    const int count = min(rows - 16 * i, 16) * R;
+    for (int q = threadIdx.x; q < count; q += 64 * kWaves) {
+      float s = red[0][q];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s += red[w][q];
+      out[16 * i * R + q] = q % R < rk ? f * s : 0.0f;
+    }
   }
 }
 
@@ -183,7 +203,10 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
 // written in whole 256-byte runs, 16 bytes a lane.  The factor's rows lie along
 // the columns, so a lane reads eight rows (k) of its CW columns and exchanges
 // halves between them to get CW operands; they stay in registers while the
-// workgroup walks over its 16 TT tokens.  The sums start from Y0.
+// workgroup walks over its 16 TT tokens.  V's operands are the same for every
+// column: the workgroup adds up the low kernel's parts and splits them once,
+// into LDS, in the order the matrix instructions take them.  The sums start
+// from Y0, whose next rows are loaded before the products of those in hand.
 
 template <class T>
 struct YRow;
@@ -213,117 +236,153 @@ struct YRow<bf16_t> {
 template <class Y, int RT, int TT>
 __global__ __launch_bounds__(64 * kWaves) void adapter_spread_kernel(int n, int d, int col_wgs,
                                                                      const float* __restrict__ part, int splits,
-                                                                     int nseg,
-                                                                     const int* __restrict__ off,
+                                                                     int nseg, const int* __restrict__ off,
                                                                      const int* __restrict__ ids, int nad,
                                                                      const bf16_t* __restrict__ factor,
                                                                      const int* __restrict__ rank, const Y* y0,
                                                                      int64_t ld0, Y* y, int64_t ldy,
                                                                      float* __restrict__ V) {
   constexpr int R = 16 * RT, T = 16 * TT, KS = (R + 31) / 32, CW = YRow<Y>::CW;
+  // Operands of one 16-token tile and 32 ranks: three terms.  At rank 16 the
+  // upper half of k is free, and the first two terms share one operand (against
+  // the factor's rows twice).
+  constexpr int TERMS = RT == 1 ? 2 : 3;
   using raw = typename YRow<Y>::raw;
+  using factors = typename YRow<Y>::factors;
+  __shared__ u32x4 vop[TT][KS][TERMS][64];
   const int col_wg = blockIdx.x % col_wgs;
   const Tile t = find_tile<T>(blockIdx.x / col_wgs, n, nseg, off, ids, nad);
   if (t.begin >= t.end) return;
-  const int rows = t.end - t.begin;
-  const int64_t v_step = static_cast<int64_t>(n) * R;
-  // V itself, where the caller keeps it: the first column workgroup writes it
-  if (V && col_wg == 0) {
-    const int64_t b = static_cast<int64_t>(t.begin) * R;
-    for (int i = threadIdx.x; i < rows * R; i += 64 * kWaves) {
-      float s = part[b + i];
-      for (int p = 1; p < splits; ++p) s += part[b + p * v_step + i];
-      V[b + i] = s;
-    }
-  }
+  const int rows = t.end - t.begin, tiles = (rows + 15) / 16;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c0 = (col_wg * kWaves + wave) * 16 * CW;
-  if (c0 >= d) return;
   // lanes past the last column repeat it and store nothing: the matrix
   // instructions take their token rows from every lane
-  const bool in_c = c0 + CW * j < d;
-  const int c = in_c ? c0 + CW * j : d - CW;
+  int c0 = (col_wg * kWaves + wave) * 16 * CW, c = min(c0 + CW * j, d - CW);
   const int rk = t.adapter < 0 ? 0 : min(max(rank[t.adapter], 0), R);
-  u32x4 w[KS][CW];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    if (32 * ks >= rk) {
-#pragma unroll
-      for (int i = 0; i < CW; ++i) w[ks][i] = u32x4{0u, 0u, 0u, 0u};
-      continue;
-    }
-    typename YRow<Y>::factors in[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = min(32 * ks + 8 * g + i, rk - 1);
-      in[i] = *reinterpret_cast<const typename YRow<Y>::factors*>(
-          factor + (static_cast<int64_t>(t.adapter) * R + r) * d + c);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int q = 0; q < CW / 2; ++q)
-        if (32 * ks + 8 * g + i >= rk) in[i][q] = 0u;
-#pragma unroll
-    for (int i = 0; i < CW; ++i)
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        w[ks][i][p] = __builtin_amdgcn_perm(in[2 * p + 1][i / 2], in[2 * p][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-  }
-  for (int i = 0; i < TT; ++i) {
-    if (16 * i >= rows) break;
-    YRow<Y> in[4];
+  raw in[4];
+  auto load_rows = [&](int i) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t row = min(t.begin + 16 * i + 4 * g + e, t.end - 1);
-      if (y0)
-        in[e].v = *reinterpret_cast<const raw*>(y0 + row * ld0 + c);
-      else
-        in[e].v = raw{0, 0, 0, 0};
+      in[e] = y0 ? *reinterpret_cast<const raw*>(y0 + row * ld0 + c) : raw{0, 0, 0, 0};
     }
-    f32x4 acc[CW];
+  };
+  factors fr[KS][8];
+  auto load_factor = [&]() {
 #pragma unroll
-    for (int q = 0; q < CW; ++q) acc[q] = f32x4{in[0].at(q), in[1].at(q), in[2].at(q), in[3].at(q)};
-    if (rk > 0) {
-      const float* vp = part + static_cast<int64_t>(min(t.begin + 16 * i + j, t.end - 1)) * R + 8 * g;
+    for (int ks = 0; ks < KS; ++ks) {
+      if (32 * ks >= rk) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
+        fr[ks][i] = *reinterpret_cast<const factors*>(
+            factor + (static_cast<int64_t>(t.adapter) * R + min(r, rk - 1)) * d + c);
+      }
+    }
+  };
+  load_rows(0);
+  load_factor();
+  if (rk > 0 || V) {
+    const int64_t v_step = static_cast<int64_t>(n) * R;
+    for (int q = threadIdx.x; q < tiles * 16 * (R / 8); q += 64 * kWaves) {
+      const int row = q / (R / 8), r8 = q % (R / 8);
+      float v[8] = {};
+      if (row < rows) {
+        const float* p = part + (static_cast<int64_t>(t.begin) + row) * R + 8 * r8;
+        raw8<float> r;
+        load8(r, p);
+        widen8(r, v);
+#pragma unroll 4
+        for (int i = 1; i < splits; ++i) {
+          float o[8];
+          load8(r, p + i * v_step);
+          widen8(r, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += o[k];
+        }
+        // V itself, where the caller keeps it
+        if (V && col_wg == 0) store8(V + (static_cast<int64_t>(t.begin) + row) * R + 8 * r8, v);
+      }
+      u32x4 o[3];
+      split8(v, o);
+      u32x4(*to)[64] = vop[row / 16][r8 / 4];
+      const int at = 16 * (r8 & 3) + (row & 15);
+      if constexpr (RT == 1) {
+        to[0][at] = o[0];
+        to[0][at + 32] = o[1];
+        to[1][at] = o[2];
+        to[1][at + 32] = u32x4{0u, 0u, 0u, 0u};
+      } else {
+#pragma unroll
+        for (int m = 0; m < 3; ++m) to[m][at] = o[m];
+      }
+    }
+    __syncthreads();
+  }
+  if (c0 >= d) return;
+  const int stride = col_wgs * kWaves * 16 * CW;
+  // the factor rows of the next columns too, where the registers hold both
+  constexpr bool kAhead = TT == 1 && KS * CW <= 16;
+  for (bool again = false;; again = true) {
+    if (TT == 1 && !kAhead && again) load_factor();
+    u32x4 w[KS][CW];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (32 * ks >= rk) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
+#pragma unroll
+        for (int q = 0; q < CW / 2; ++q)
+          if (r >= rk) fr[ks][i][q] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < CW; ++i)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          w[ks][i][p] = __builtin_amdgcn_perm(fr[ks][2 * p + 1][i / 2], fr[ks][2 * p][i / 2],
+                                              i & 1 ? 0x07060302u : 0x05040100u);
+    }
+    const int c_now = c;
+    const bool in_c = c0 + CW * j < d, more = TT == 1 && c0 + stride < d;
+    for (int i = 0; i < tiles; ++i) {
+      f32x4 acc[CW];
+      YRow<Y> b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e].v = in[e];
+#pragma unroll
+      for (int q = 0; q < CW; ++q) acc[q] = f32x4{b[0].at(q), b[1].at(q), b[2].at(q), b[3].at(q)};
+      if (i + 1 < tiles) {
+        load_rows(i + 1);
+      } else if (more) {
+        c0 += stride;
+        c = min(c0 + CW * j, d - CW);
+        if constexpr (kAhead) load_factor();
+        load_rows(0);
+      }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         if (32 * ks >= rk) break;
-        float v[8];
-        const bool in_r = 32 * ks + 8 * g < R;
-        raw8<float> r;
-        load8(r, vp + (in_r ? 32 * ks : -8 * g));
-        widen8(r, v);
-        for (int p = 1; p < splits; ++p) {
-          float o[8];
-          load8(r, vp + p * v_step + (in_r ? 32 * ks : -8 * g));
-          widen8(r, o);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] += o[q];
+        for (int m = 0; m < TERMS; ++m) {
+          const u32x4 v = vop[i][ks][m][lane];
+#pragma unroll
+          for (int q = 0; q < CW; ++q) acc[q] = mfma(v, w[ks][q], acc[q]);
         }
-        if (!in_r) {
+      }
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-        }
-        u32x4 vt[3];
-        split8(v, vt);
+      for (int e = 0; e < 4; ++e) {
+        const int row = t.begin + 16 * i + 4 * g + e;
+        float s[CW];
 #pragma unroll
-        for (int m = 0; m < 3; ++m)
-#pragma unroll
-          for (int q = 0; q < CW; ++q) acc[q] = mfma(vt[m], w[ks][q], acc[q]);
+        for (int q = 0; q < CW; ++q) s[q] = acc[q][e];
+        YRow<Y> o;
+        o.put(s);
+        if (in_c && row < t.end) *reinterpret_cast<raw*>(y + row * ldy + c_now) = o.v;
       }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = t.begin + 16 * i + 4 * g + e;
-      float s[CW];
-#pragma unroll
-      for (int q = 0; q < CW; ++q) s[q] = acc[q][e];
-      YRow<Y> o;
-      o.put(s);
-      if (in_c && row < t.end) *reinterpret_cast<raw*>(y + row * ldy + c) = o.v;
-    }
+    if (!more) break;
   }
 }
 
@@ -388,8 +447,12 @@ void spread_by_tiles(bool one, int n, int d, const float* part, int splits, int 
                      int nad, const void* factor, const int* rank, const void* y0, int64_t ld0, void* y, int64_t ldy,
                      float* V, hipStream_t s) {
   const int cols = 16 * YRow<Y>::CW * kWaves, tokens = one ? 16 : 64;
-  const int col_wgs = (d + cols - 1) / cols;
-  const dim3 grid(static_cast<unsigned>(col_wgs * tile_numbers(n, tokens, nseg)));
+  // short requests: a workgroup takes several column blocks in turn, so that
+  // at most four for every compute unit (one round of them) do it all
+  const int64_t tiles = tile_numbers(n, tokens, nseg);
+  const int all = (d + cols - 1) / cols, few = tiles < 1024 ? static_cast<int>(1024 / tiles) : 1;
+  const int col_wgs = one && few < all ? few : all;
+  const dim3 grid(static_cast<unsigned>(col_wgs * tiles));
   auto k = one ? adapter_spread_kernel<Y, RT, 1> : adapter_spread_kernel<Y, RT, 4>;
   hipLaunchKernelGGL(k, grid, dim3(64 * kWaves), 0, s, n, d, col_wgs, part, splits, nseg, off, ids, nad,
                      static_cast<const bf16_t*>(factor), rank, static_cast<const Y*>(y0), ld0, static_cast<Y*>(y), ldy,
@@ -415,7 +478,6 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kMaxSeg = 1 << 20;
 constexpr int kMaxTokens = 1 << 24;   // so that sums over 64 requests stay in 32 bits
-
 // X as the grad kernel sees it: the two float types and the act8 codes.
 constexpr int kAct8 = 2;
 
@@ -502,7 +564,7 @@ extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wus
   if (ldg < d_out || ldg % 8 || ldx < d_in || ldx % 8 || (dX && (lddx < d_in || lddx % 8)) ||
       (dX && dX0 && (lddx0 < d_in || lddx0 % 8)))
     return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
-  if (!adapter_grads_fit(n, d_in, d_out, nad)) return fail(WUSH_E_SHAPE, "%s: nad=%d passes the launch limit", who, nad);
+  if (!adapter_grads_fit(n, d_in, d_out, nad, rmax)) return fail(WUSH_E_SHAPE, "%s: nad=%d passes the launch limit", who, nad);
   if (x_scales && (d_in % 32 || ldx != d_in))
     return fail(WUSH_E_SHAPE, "%s: an act8 checkpoint has whole groups of 32 and no row stride of its own", who);
   if (!seg_off || !seg_adapter || !A || !Bt || !rank || !alpha || !dA || !dBt || (n > 0 && (!dY || !X || !V)))
@@ -521,9 +583,9 @@ extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wus
   float* part = static_cast<float*>(base);
   float* dV = reinterpret_cast<float*>(static_cast<char*>(base) + round256(part_bytes(n, d_out, nseg, rmax)));
   char* rest = reinterpret_cast<char*>(dV) + round256(static_cast<size_t>(n) * rmax * sizeof(float));
+  const int splits = low_splits(n, d_out, nseg, rmax);
   wush_status out = WUSH_OK;
   if (n > 0) {
-    const int splits = low_splits(n, d_out, nseg, rmax);
     auto f = gdt == WUSH_F32 ? low<float> : low<bf16_t>;
     f(n, d_out, dY, ldg, nseg, seg_off, seg_adapter, nad, rmax, Bt, rank, alpha, part, s);
     out = launched(who);

@@ -3,19 +3,20 @@
 //
 // The sum runs over tokens, which lie along the slow axis of both operands, and
 // an adapter's tokens may be spread over many requests.  A first small kernel
-// lists the tokens of each adapter in order (`tokens`), and cuts each list into
-// chunks; the grad kernel takes one chunk and 128 columns per workgroup.
+// lists the tokens of each adapter in order, each list padded to whole steps of
+// 32 tokens, and cuts it into chunks of several steps; a last one adds up the
+// chunks of an adapter in order, so that results do not depend on scheduling
+// (an adapter of one chunk is written directly).
 //
 // In a 16x16x32 product the eight k values of a lane are eight tokens.  A lane
 // therefore loads the same eight columns of eight token rows, 16 bytes each
 // (16 lanes read 256 contiguous bytes of a row), and exchanges halves between
-// its own registers; no LDS and no lane exchange is needed, since which column
-// a result belongs to is free to choose: operand c of lane j is column 8 j + c.
-// The same holds for the rows: S is read as RT neighbouring values per lane, and
-// row tile rt holds the rows RT j + rt.
-//
-// Chunks of one adapter are summed in order by a third kernel, so the result
-// does not depend on scheduling; an adapter of one chunk is written directly.
+// its own registers; no lane exchange is needed, since which column a result
+// belongs to is free to choose: operand c of lane j is column 8 j + c.  A wave
+// owns 128 columns.  The four waves of a workgroup walk over the same tokens
+// and share the operands of S, which they split into three bf16 terms together,
+// one step ahead, through two LDS buffers.  The rows of X are loaded one step
+// ahead too, into the registers that the step's operands have just left.
 
 #include <hip/hip_runtime.h>
 
@@ -29,16 +30,21 @@ using namespace wush;
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kCols = 128;
+constexpr int kCols = 128 * kWaves;
 
-// tokens [n]: the tokens of adapter 0, 1, ... in request order
-// start [nad + 1]: where an adapter's tokens begin in that list
+// tokens [whole steps]: the tokens of adapter 0, 1, ..., each list in request
+//   order and padded to a multiple of 32 by its last token
+// count [nad]: an adapter's tokens (0 where its rank is)
+// start [nad + 1]: where its list begins, a multiple of 32
 // chunk [nad + 1]: the number of its first chunk
+// span [nad]: tokens of its chunks, whole steps
 // place [nseg]: where a request's tokens begin
 struct Lists {
   int* tokens;
+  int* count;
   int* start;
   int* chunk;
+  int* span;
   int* place;
 };
 
@@ -52,9 +58,17 @@ __device__ __forceinline__ int lane_prefix(int v) {   // inclusive
   return v;
 }
 
+// Steps of a chunk at least, and the relative cost of a step: what the rows
+// take, and the products of each row tile.
+constexpr int kMinSteps = 4;
+__device__ __forceinline__ float step_cost(int rank, int rmax) {
+  const int tiles = (min(max(rank, 1), rmax) + 15) / 16;
+  return tiles > 4 ? 9.0f : tiles > 2 ? 6.0f : tiles > 1 ? 5.0f : 4.5f;
+}
+
 __global__ __launch_bounds__(1024) void adapter_list_kernel(int n, int nseg, const int* __restrict__ off,
                                                             const int* __restrict__ ids, int nad,
-                                                            const int* __restrict__ rank, int span, Lists l) {
+                                                            const int* __restrict__ rank, int rmax, int chunks_wanted, Lists l) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   auto length = [&](int s, int a) {
     if (s >= nseg || ids[s] != a) return 0;
@@ -66,50 +80,81 @@ __global__ __launch_bounds__(1024) void adapter_list_kernel(int n, int nseg, con
     if (rank[a] > 0)
       for (int b = 0; b < nseg; b += 64) sum = min(sum + length(b + lane, a), n);
     sum = __shfl(lane_prefix(sum), 63, 64);
-    if (lane == 0) l.start[a] = min(sum, n);
+    if (lane == 0) l.count[a] = min(sum, n);
   }
   __syncthreads();
   if (wave == 0) {
-    int tokens = 0, chunks = 0;
+    // a list's cost: its tokens times the cost of a step at its rank
+    float cost = 0.0f;
+    int busy = 0;
+    for (int a = lane; a < nad; a += 64) {
+      cost += l.count[a] * step_cost(rank[a], rmax);
+      busy += l.count[a] > 0;
+    }
+    cost = wave_sum(cost);
+    busy = __shfl(lane_prefix(busy), 63, 64);
+    // every list ends inside a chunk, half of one wasted on average
+    const float share = cost / max(1, chunks_wanted - busy / 2);
+    int tokens = 0, chunks = 0, steps = 0;   // tokens: those that are not padding
     for (int b = 0; b < nad; b += 64) {
       const int a = b + lane;
       // capped at n, which offsets that do not rise could pass
-      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(a < nad ? l.start[a] : 0));
+      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(a < nad ? l.count[a] : 0));
       const int to = static_cast<int>(min(past, static_cast<int64_t>(n)));
-      const int before = __shfl_up(to, 1, 64), from = lane == 0 ? tokens : before;
-      const int parts = (to - from + span - 1) / span, c = lane_prefix(parts);
+      const int before = __shfl_up(to, 1, 64);
+      const int mine = to - (lane == 0 ? tokens : before);
+      const int span = a < nad ? 32 * max(kMinSteps, static_cast<int>(ceilf(share / (32.0f * step_cost(rank[a], rmax))))) : 32;
+      const int parts = (mine + span - 1) / span, c = lane_prefix(parts);
+      const int turns = (mine + 31) / 32, t = lane_prefix(turns);
       if (a < nad) {
-        l.start[a] = from;
+        l.count[a] = mine;
+        l.span[a] = span;
+        l.start[a] = 32 * (steps + t - turns);
         l.chunk[a] = chunks + c - parts;
       }
       tokens = __shfl(to, 63, 64);
+      steps += __shfl(t, 63, 64);
       chunks += __shfl(c, 63, 64);
     }
     if (lane == 0) {
-      l.start[nad] = tokens;
+      l.start[nad] = 32 * steps;
       l.chunk[nad] = chunks;
     }
   }
   __syncthreads();
   for (int a = wave; a < nad; a += 16) {
-    if (rank[a] <= 0) continue;
-    int at = l.start[a];
+    const int room = l.count[a];
+    if (room == 0) continue;
+    int at = 0;
     for (int b = 0; b < nseg; b += 64) {
       const int m = length(b + lane, a), p = lane_prefix(m);
-      if (m > 0) l.place[b + lane] = at + p - m;
-      at = min(at + __shfl(p, 63, 64), n);
+      if (m > 0) l.place[b + lane] = min(at + p - m, room);
+      at = min(at + __shfl(p, 63, 64), room);
     }
   }
   __syncthreads();
   for (int s = wave; s < nseg; s += 16) {
     const int a = ids[s];
-    if (a < 0 || a >= nad || rank[a] <= 0) continue;
+    if (a < 0 || a >= nad || l.count[a] == 0) continue;
     const int first = request_start(off, s, nseg, n), m = request_start(off, s + 1, nseg, n) - first;
     if (m <= 0) continue;
-    const int at = l.place[s];
-    for (int i = lane; i < m; i += 64)
-      if (at + i < n) l.tokens[at + i] = first + i;
+    const int start = l.start[a], room = l.count[a], at = l.place[s];
+    for (int i = lane; i < m && at + i < room; i += 64) {
+      l.tokens[start + at + i] = first + i;
+      if (at + i == room - 1)
+        for (int q = room; q < (room + 31) / 32 * 32; ++q) l.tokens[start + q] = first + i;
+    }
   }
+}
+
+// Adapter of a step or chunk `number`: the last one whose first is not past it.
+__device__ __forceinline__ int owner(const int* __restrict__ firsts, int nad, int number) {
+  int count = 0;
+  for (int b = 0; b < nad; b += 64) {
+    const int i = b + (threadIdx.x & 63);
+    count += __popcll(__ballot(i < nad && firsts[i < nad ? i : 0] <= number));
+  }
+  return __builtin_amdgcn_readfirstlane(count - 1);
 }
 
 // Eight columns of eight token rows, and the matrix operands of each column.
@@ -125,9 +170,8 @@ struct Rows<bf16_t> {
   __device__ __forceinline__ void load(int i, const void* x, const uint8_t*, int64_t row, int64_t ld, int c) {
     v[i] = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(x) + row * ld + c);
   }
-  __device__ __forceinline__ void clear(int i) { v[i] = u32x4{0u, 0u, 0u, 0u}; }
   __device__ __forceinline__ void prepare() {}
-  __device__ __forceinline__ void column(int c, u32x4 (&t)[3]) const {
+  __device__ __forceinline__ void column(int c, u32x4 (&t)[1]) const {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
       t[0][p] = __builtin_amdgcn_perm(v[2 * p + 1][c / 2], v[2 * p][c / 2], c & 1 ? 0x07060302u : 0x05040100u);
@@ -141,8 +185,6 @@ struct Rows<float> {
   __device__ __forceinline__ void load(int i, const void* x, const uint8_t*, int64_t row, int64_t ld, int c) {
     load8(v[i], static_cast<const float*>(x) + row * ld + c);
   }
-  __device__ __forceinline__ void clear(int i) { v[i] = raw8<float>{}; }
-  __device__ __forceinline__ void prepare() {}
   __device__ __forceinline__ void column(int c, u32x4 (&t)[3]) const {
     float x[8];
 #pragma unroll
@@ -157,47 +199,33 @@ struct Rows<act8_t> {
   static constexpr int kTerms = 1;
   u32x2 v[8];
   uint32_t byte[8];
-  float m[8];
   __device__ __forceinline__ void load(int i, const void* x, const uint8_t* scales, int64_t row, int64_t ld, int c) {
     v[i] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(x) + row * ld + c);
     byte[i] = scales[row * (ld / 32) + c / 32];
   }
-  __device__ __forceinline__ void clear(int i) {
-    v[i] = u32x2{0u, 0u};
-    byte[i] = 127u;
-  }
+  // The scale bytes as 2^(e-6).  A byte of 255 stands for NaN, and is rare: one
+  // look at the largest decides.
   __device__ __forceinline__ void prepare() {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, byte[i]);
+    const bool bad = __ballot(top == 255u) != 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t s = byte[i] == 255u ? 0x7fc00000u : (max(byte[i], 6u) - 6u) << 23;
-      m[i] = __builtin_bit_cast(float, s);
+      const uint32_t unit = (byte[i] << 23) - (6u << 23);
+      byte[i] = bad && byte[i] == 255u ? 0x7fc00000u : unit;
     }
   }
-  __device__ __forceinline__ void column(int c, u32x4 (&t)[3]) const {
+  __device__ __forceinline__ void column(int c, u32x4 (&t)[1]) const {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      x[i] = static_cast<float>(static_cast<int8_t>(v[i][c / 4] >> (8 * (c & 3)))) * m[i];
+      x[i] = static_cast<float>(static_cast<int8_t>(v[i][c / 4] >> (8 * (c & 3)))) * __builtin_bit_cast(float, byte[i]);
 #pragma unroll
     for (int p = 0; p < 4; ++p)
       t[0][p] = top_halves(__builtin_bit_cast(uint32_t, x[2 * p]), __builtin_bit_cast(uint32_t, x[2 * p + 1]));
   }
 };
-
-template <int RT>
-__device__ __forceinline__ void load_rank(const float* p, float* v) {
-  if constexpr (RT >= 4) {
-#pragma unroll
-    for (int q = 0; q < RT / 4; ++q) {
-      const f32x4 r = reinterpret_cast<const f32x4*>(p)[q];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] = r[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) v[i] = p[i];
-  }
-}
 
 struct Side {
   const void* x;
@@ -209,143 +237,222 @@ struct Side {
   int d;
 };
 
-template <class X, int RT>
-__device__ __forceinline__ void grad_tile(const Side& side, int col_wg, int begin, int end, int rk,
-                                          const int* __restrict__ tokens, float* __restrict__ out,
-                                          float (*red)[RT * 4 * 64]) {
-  constexpr int R = 16 * RT;
+// Keeps the scheduler from moving loads and operands of one part of a step into
+// another, which costs more registers than there are.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Operands of S for one step: row tile, term, lane.
+template <int RT>
+using Shared = u32x4[RT][3][64];
+
+// Steps [first, last) of an adapter whose list ends at `end`, for NT of the RT
+// row tiles.
+template <class X, int NT, int RT>
+__device__ __forceinline__ void grad_steps(const Side& side, int c, int first, int last, int end,
+                                           const int* __restrict__ tokens, Shared<RT>* ops, f32x4 (&acc)[RT][8]) {
+  constexpr int R = 16 * RT, kTerms = Rows<X>::kTerms, kShare = (NT + kWaves - 1) / kWaves;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = col_wg * kCols + 8 * j;
-  const int c = min(col, side.d - 8);
+  Rows<X> x;
+  float v[kShare][8];
+  // a step's tokens are one per lane (twice); a lane's own are 8 g .. 8 g + 7
+  auto list = [&](int step) { return tokens[32 * step + (lane & 31)]; };
+  auto load_x = [&](int token) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.load(i, side.x, side.scales, __shfl(token, 8 * g + i, 64), side.ld, c);
+  };
+  // S of the row tiles that this wave prepares
+  auto load_s = [&](int token) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float* p = side.s + static_cast<int64_t>(__shfl(token, 8 * g + i, 64)) * R + j;
+#pragma unroll
+      for (int w = 0; w < kShare; ++w)
+        if (wave + w * kWaves < NT) v[w][i] = p[16 * (wave + w * kWaves)];
+    }
+  };
+  auto share = [&](int step, Shared<RT>& to) {
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) {
+      const int r = wave + w * kWaves;
+      if (r >= NT) break;
+      if (32 * (step + 1) > end) {   // padding
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (32 * step + 8 * g + i >= end) v[w][i] = 0.0f;
+      }
+      u32x4 o[3];
+      split8(v[w], o);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) to[r][m][lane] = o[m];
+    }
+  };
+  int token = list(first), ahead = first + 1 < last ? list(first + 1) : 0;
+  load_s(token);
+  if constexpr (kTerms == 1) load_x(token);
+  share(first, ops[0]);
+  __syncthreads();
+  for (int step = first, buf = 0; step < last; ++step, buf ^= 1) {
+    const bool more = step + 1 < last;
+    u32x4 xt[8][1];
+    if constexpr (kTerms == 1) {
+      x.prepare();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x.column(q, xt[q]);
+      fence();
+    } else {
+      load_x(token);
+    }
+    if (more) {
+      token = ahead;
+      load_s(token);
+      if constexpr (kTerms == 1) load_x(token);
+      if (step + 2 < last) ahead = list(step + 2);
+    }
+    if constexpr (kTerms == 1) {
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        fence();
+        u32x4 st[NT];
+#pragma unroll
+        for (int r = 0; r < NT; ++r) st[r] = ops[buf][r][m][lane];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int r = 0; r < NT; ++r) acc[r][q] = mfma(st[r], xt[q][0], acc[r][q]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        u32x4 t[3];
+        x.column(q, t);
+        // of three terms by three, those above 2^-24 of the product
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int r = 0; r < NT; ++r) {
+            const u32x4 st = ops[buf][r][m][lane];
+#pragma unroll
+            for (int k = 0; k < 3 - m; ++k) acc[r][q] = mfma(st, t[k], acc[r][q]);
+          }
+      }
+    }
+    fence();
+    if (more) share(step + 1, ops[buf ^ 1]);
+    __syncthreads();
+  }
+}
+
+template <class X, int RT>
+__device__ __forceinline__ void grad_tile(const Side& side, int c0, int first, int last, int end, int rk,
+                                          int rows, const int* __restrict__ tokens, Shared<RT>* ops,
+                                          float* __restrict__ out) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  // waves and lanes past the last column repeat it: they still share the work
+  // on S, and store nothing
+  const int col = c0 + 8 * j, c = min(col, side.d - 8);
   f32x4 acc[RT][8];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[r][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int t0 = begin + 32 * wave; t0 < end; t0 += 32 * kWaves) {
-    Rows<X> x;
-    float s[8][RT];
-    const bool whole = t0 + 32 <= end;
+  // row tiles in use, rounded up to a power of two; the extra ones are zero in S
+  const int tiles = (rk + 15) / 16;
+  if (RT > 4 && tiles > 4)
+    grad_steps<X, RT, RT>(side, c, first, last, end, tokens, ops, acc);
+  else if (RT > 2 && tiles > 2)
+    grad_steps<X, (RT > 4 ? 4 : RT), RT>(side, c, first, last, end, tokens, ops, acc);
+  else if (RT > 1 && tiles > 1)
+    grad_steps<X, (RT > 2 ? 2 : RT), RT>(side, c, first, last, end, tokens, ops, acc);
+  else
+    grad_steps<X, 1, RT>(side, c, first, last, end, tokens, ops, acc);
+  if (col >= side.d) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = tokens[min(t0 + 8 * g + i, end - 1)];
-      x.load(i, side.x, side.scales, row, side.ld, c);
-      load_rank<RT>(side.s + row * R + RT * j, s[i]);
-    }
-    if (!whole) {
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (t0 + 8 * g + i >= end) {
-          x.clear(i);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) s[i][r] = 0.0f;
-        }
-    }
-    x.prepare();
-    u32x4 st[RT][3];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int e = 0; e < 4; ++e) {
+      const int row = 16 * r + 4 * g + e;
+      if (row >= rows) continue;
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = s[i][r];
-      split8(v, st[r]);
+      for (int q = 0; q < 8; ++q) v[q] = row < rk ? acc[r][q][e] : 0.0f;
+      store8(out + static_cast<int64_t>(row) * side.d + col, v);
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      u32x4 xt[3];
-      x.column(q, xt);
-      // of three terms by three, those above 2^-24 of the product
-#pragma unroll
-      for (int m = 0; m < 3; ++m)
-#pragma unroll
-        for (int k = 0; k < Rows<X>::kTerms; ++k) {
-          if (m + k > 2) continue;
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r][q] = mfma(st[r][m], xt[k], acc[r][q]);
-        }
-    }
-  }
-  // the four waves' sums, one column operand at a time: wave w writes its
-  // share of every column, then sums two of the eight columns over the waves
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][(r * 4 + e) * 64 + lane] = acc[r][q][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < RT * 4 * 64; i += 64 * kWaves) {
-      const int l = i & 63, re = i >> 6;
-      const int row = RT * (4 * (l >> 4) + (re & 3)) + (re >> 2), cc = col_wg * kCols + 8 * (l & 15) + q;
-      float sum = red[0][i];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) sum += red[w][i];
-      if (cc < side.d) out[static_cast<int64_t>(row) * side.d + cc] = row < rk ? sum : 0.0f;
-    }
-  }
 }
 
+// Two waves a SIMD up to rank 64, whose accumulators take half of the registers.
 template <class X, class G, int RT>
-__global__ __launch_bounds__(64 * kWaves) void adapter_grad_kernel(Side a, Side b, int wgs_a, int nad,
-                                                                   const int* __restrict__ rank, int span, Lists l) {
+__global__ __launch_bounds__(64 * kWaves, RT > 4 ? 1 : 2) void adapter_grad_kernel(Side a, Side b, int wgs_a, int nad,
+                                                                   const int* __restrict__ rank, Lists l) {
   constexpr int R = 16 * RT;
-  __shared__ float red[kWaves][RT * 4 * 64];
+  __shared__ Shared<RT> ops[2];
   const int number = blockIdx.y;
   if (number >= l.chunk[nad]) return;
-  int count = 0;
-  for (int base = 0; base < nad; base += 64) {
-    const int i = base + (threadIdx.x & 63);
-    count += __popcll(__ballot(i < nad && l.chunk[i < nad ? i : 0] <= number));
-  }
-  const int ad = __builtin_amdgcn_readfirstlane(count - 1);
-  const int first = l.chunk[ad], chunks = l.chunk[ad + 1] - first;
-  const int begin = l.start[ad] + (number - first) * span, end = min(l.start[ad + 1], begin + span);
+  const int ad = owner(l.chunk, nad, number);
+  const int before = l.chunk[ad], chunks = l.chunk[ad + 1] - before;
+  const int span = l.span[ad];
+  const int first = l.start[ad] + (number - before) * span, last = min(l.start[ad + 1], first + span);
   const int rk = min(rank[ad], R);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool left = blockIdx.x < wgs_a;
   const int64_t size = static_cast<int64_t>(R) * (left ? a.d : b.d);
   float* out = chunks == 1 ? (left ? a.out : b.out) + ad * size : (left ? a.part : b.part) + number * size;
+  const int c0 = (left ? blockIdx.x : blockIdx.x - wgs_a) * kCols + 128 * wave;
+  const int end = l.start[ad] + l.count[ad];
+  // rows that do not count are left out of the chunks' parts
+  const int rows = chunks == 1 ? R : rk;
   if (left)
-    grad_tile<X, RT>(a, blockIdx.x, begin, end, rk, l.tokens, out, red);
+    grad_tile<X, RT>(a, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, out);
   else
-    grad_tile<G, RT>(b, blockIdx.x - wgs_a, begin, end, rk, l.tokens, out, red);
+    grad_tile<G, RT>(b, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, out);
 }
 
-// Sums the chunks of the adapters that have several, clears those of none.
-__global__ __launch_bounds__(256) void adapter_join_kernel(Side a, Side b, int R, int nad, Lists l) {
+// Sums the chunks of the adapters that have several, clears those of none and
+// the rows that do not count.
+__global__ __launch_bounds__(256) void adapter_join_kernel(Side a, Side b, int R, int nad,
+                                                           const int* __restrict__ rank, Lists l) {
   const int ad = blockIdx.y;
   const int first = l.chunk[ad], last = l.chunk[ad + 1];
   if (last - first == 1) return;
   const bool left = blockIdx.z == 0;
   const float* part = left ? a.part : b.part;
   float* out = left ? a.out : b.out;
-  const int64_t count = static_cast<int64_t>(R) * (left ? a.d : b.d);
+  const int d = left ? a.d : b.d;
+  const int64_t count = static_cast<int64_t>(R) * d, used = static_cast<int64_t>(min(max(rank[ad], 0), R)) * d;
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < count;
        i += static_cast<int64_t>(gridDim.x) * 1024) {
     f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = first; k < last; ++k) s += *reinterpret_cast<const f32x4*>(part + k * count + i);
+    if (i < used) {
+#pragma unroll 4
+      for (int k = first; k < last; ++k) s += *reinterpret_cast<const f32x4*>(part + k * count + i);
+    }
     *reinterpret_cast<f32x4*>(out + ad * count + i) = s;
   }
 }
 
-// Tokens per chunk: so many that the grid has about four workgroups for every
-// compute unit, in whole turns of the four waves (128 tokens).
-int span_of(int n, int d_in, int d_out) {
+// Chunks wanted: so many that the workgroups fit the compute units once (two on
+// each; three at rank 16, one at rank 128), since a second round for the last
+// few would take as long as the first.
+int chunks_wanted(int n, int d_in, int d_out, int rmax) {
   const int wgs = (d_in + kCols - 1) / kCols + (d_out + kCols - 1) / kCols;
-  const int chunks = (1024 + wgs - 1) / wgs;
-  const int span = (n + chunks - 1) / chunks;
-  return (span + 127) / 128 * 128 > 0 ? (span + 127) / 128 * 128 : 128;
+  const int slots = rmax == 16 ? 768 : rmax == 128 ? 256 : 512;
+  const int least = n / (32 * kMinSteps) + 1;
+  const int c = slots / wgs;
+  return c < 1 ? 1 : c < least ? c : least;
 }
 
-int64_t chunk_numbers(int n, int span, int nad) { return static_cast<int64_t>(n / span) + nad; }
+// Chunks there may be: each list's last may be short.
+int64_t chunk_numbers(int n, int d_in, int d_out, int nad, int rmax) {
+  return static_cast<int64_t>(chunks_wanted(n, d_in, d_out, rmax)) + nad;
+}
+int64_t step_numbers(int n, int nad) { return static_cast<int64_t>(n / 32) + nad; }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 template <class X, class G, int RT>
-void launch(dim3 grid, const Side& a, const Side& b, int wgs_a, int nad, const int* rank, int span, const Lists& l,
+void launch(dim3 grid, const Side& a, const Side& b, int wgs_a, int nad, const int* rank, const Lists& l,
             hipStream_t s) {
-  hipLaunchKernelGGL((adapter_grad_kernel<X, G, RT>), grid, dim3(64 * kWaves), 0, s, a, b, wgs_a, nad, rank, span, l);
+  hipLaunchKernelGGL((adapter_grad_kernel<X, G, RT>), grid, dim3(64 * kWaves), 0, s, a, b, wgs_a, nad, rank, l);
 }
 
 template <class X, class G>
@@ -358,36 +465,38 @@ auto by_rank(int rmax) {
 namespace wush {
 
 size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax) {
-  const int span = span_of(n, d_in, d_out);
-  return round256(static_cast<size_t>(n) * 4) + 2 * round256((static_cast<size_t>(nad) + 1) * 4) +
+  return round256(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4) + 4 * round256((static_cast<size_t>(nad) + 1) * 4) +
          round256(static_cast<size_t>(nseg) * 4) +
-         static_cast<size_t>(chunk_numbers(n, span, nad)) * rmax * (static_cast<size_t>(d_in) + d_out) * sizeof(float);
+         static_cast<size_t>(chunk_numbers(n, d_in, d_out, nad, rmax)) * rmax * (static_cast<size_t>(d_in) + d_out) * sizeof(float);
 }
 
-bool adapter_grads_fit(int n, int d_in, int d_out, int nad) {
-  return chunk_numbers(n, span_of(n, d_in, d_out), nad) <= 0xffff;
+bool adapter_grads_fit(int n, int d_in, int d_out, int nad, int rmax) {
+  return chunk_numbers(n, d_in, d_out, nad, rmax) <= 0xffff;
 }
 
 wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int d_in, int d_out, const void* dY,
                           int64_t ldg, const void* X, const uint8_t* x_scales, int64_t ldx, int nseg,
                           const int* seg_off, const int* seg_adapter, int nad, int rmax, const int* rank,
                           const float* V, const float* dV, float* dA, float* dBt, void* ws, hipStream_t s) {
-  const int span = span_of(n, d_in, d_out);
-  const int64_t numbers = chunk_numbers(n, span, nad);
+  const int64_t numbers = chunk_numbers(n, d_in, d_out, nad, rmax);
   char* p = static_cast<char*>(ws);
+  auto take = [&](size_t bytes) {
+    char* at = p;
+    p += round256(bytes);
+    return at;
+  };
   Lists l;
-  l.tokens = reinterpret_cast<int*>(p);
-  p += round256(static_cast<size_t>(n) * 4);
-  l.start = reinterpret_cast<int*>(p);
-  p += round256((static_cast<size_t>(nad) + 1) * 4);
-  l.chunk = reinterpret_cast<int*>(p);
-  p += round256((static_cast<size_t>(nad) + 1) * 4);
-  l.place = reinterpret_cast<int*>(p);
-  p += round256(static_cast<size_t>(nseg) * 4);
+  l.tokens = reinterpret_cast<int*>(take(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4));
+  l.count = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
+  l.start = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
+  l.chunk = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
+  l.span = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
+  l.place = reinterpret_cast<int*>(take(static_cast<size_t>(nseg) * 4));
   float* part = reinterpret_cast<float*>(p);
   const Side a{X, x_scales, dV, dA, part, ldx, d_in};
   const Side b{dY, nullptr, V, dBt, part + numbers * rmax * d_in, ldg, d_out};
-  hipLaunchKernelGGL(adapter_list_kernel, dim3(1), dim3(1024), 0, s, n, nseg, seg_off, seg_adapter, nad, rank, span, l);
+  hipLaunchKernelGGL(adapter_list_kernel, dim3(1), dim3(1024), 0, s, n, nseg, seg_off, seg_adapter, nad, rank, rmax,
+                     chunks_wanted(n, d_in, d_out, rmax), l);
   const int wgs_a = (d_in + kCols - 1) / kCols, wgs_b = (d_out + kCols - 1) / kCols;
   if (n > 0) {
     const dim3 grid(wgs_a + wgs_b, static_cast<unsigned>(numbers));
@@ -395,12 +504,12 @@ wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int
     auto f = xkind == WUSH_F32 ? (g32 ? by_rank<float, float>(rmax) : by_rank<float, bf16_t>(rmax))
              : xkind == WUSH_BF16 ? (g32 ? by_rank<bf16_t, float>(rmax) : by_rank<bf16_t, bf16_t>(rmax))
                                   : (g32 ? by_rank<act8_t, float>(rmax) : by_rank<act8_t, bf16_t>(rmax));
-    f(grid, a, b, wgs_a, nad, rank, span, l, s);
+    f(grid, a, b, wgs_a, nad, rank, l, s);
   }
   const int most = d_in > d_out ? d_in : d_out;
   const int64_t wide = (static_cast<int64_t>(rmax) * most + 1023) / 1024;
   hipLaunchKernelGGL(adapter_join_kernel, dim3(static_cast<unsigned>(wide < 2048 ? wide : 2048), nad, 2), dim3(256), 0,
-                     s, a, b, rmax, nad, l);
+                     s, a, b, rmax, nad, rank, l);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? WUSH_OK : fail(WUSH_E_HIP, "%s launch: %s", who, hipGetErrorString(e));
 }

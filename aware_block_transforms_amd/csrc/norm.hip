@@ -159,11 +159,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
 // stays in registers as it lies in memory and is widened where it is used, so
 // that the columns' sums fit beside it.  MAXT: the largest workgroup, which
 // sets the registers a thread may have.
-template <class Y, class R, class U, int VPT, int MAXT, bool CHANNEL>
-__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kind, const U* __restrict__ du,
+template <class Y, class R, class U, int VPT, int MAXT, int GATE>
+__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const U* __restrict__ du,
                                                         const R* drout, const Y* __restrict__ y,
                                                         const R* __restrict__ rout, Y* __restrict__ dy, R* dr,
                                                         void* __restrict__ dgate, float* __restrict__ part) {
+  constexpr bool CHANNEL = GATE == WUSH_GATE_CHANNEL, ELEMENT = GATE == WUSH_GATE_ELEMENT;
   __shared__ float slots[2][2 * 16];
   int col[VPT];
   bool in[VPT];
@@ -179,22 +180,28 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
     }
   }
   const float inv_d = 1.0f / a.d;
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+  struct Row {
+    raw8<Y> y[VPT], g[ELEMENT ? VPT : 1];
+    raw8<R> r[VPT], d[VPT];
+    raw8<U> u[VPT];
+  };
+  auto load = [&](Row& to, int64_t row) {
     const int64_t base = row * a.d;
-    raw8<Y> ry[VPT], rg[VPT];
-    raw8<R> rr[VPT], rd[VPT];
-    raw8<U> ru[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (!in[v]) continue;
       if (a.w_pre) {
-        load8(ru[v], du + base + col[v]);
-        load8(rr[v], rout + base + col[v]);
+        load8(to.u[v], du + base + col[v]);
+        load8(to.r[v], rout + base + col[v]);
       }
-      if (drout) load8(rd[v], drout + base + col[v]);
-      if (y) load8(ry[v], y + base + col[v]);
-      if (gate_kind == WUSH_GATE_ELEMENT) load8(rg[v], static_cast<const Y*>(a.gate) + base + col[v]);
+      if (drout) load8(to.d[v], drout + base + col[v]);
+      if (y) load8(to.y[v], y + base + col[v]);
+      if (ELEMENT) load8(to.g[v], static_cast<const Y*>(a.gate) + base + col[v]);
     }
+  };
+  auto process = [&](const Row& in_row, int64_t row) {
+    const auto& [ry, rg, rr, rd, ru] = in_row;
+    const int64_t base = row * a.d;
     const float k1 = y && a.w_post ? a.k1[row] : 1.0f;
     const float k2 = a.w_pre ? a.k2[row] : 0.0f;
     float m = 0.0f;
@@ -218,7 +225,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
     }
     float sums[2] = {0.0f, 0.0f};   // p z, and the token gate's gradient
     float p[VPT][8];
-    const float gate_t = gate_kind == WUSH_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    const float gate_t = GATE == WUSH_GATE_TOKEN && a.gate ? static_cast<const float*>(a.gate)[row] : 1.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (!in[v]) continue;
@@ -253,7 +260,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
       }
       if (CHANNEL) {
         load_weights(static_cast<const float*>(a.gate), col[v], g);
-      } else if (gate_kind == WUSH_GATE_ELEMENT) {
+      } else if (ELEMENT) {
         widen8(rg[v], g);
       } else {
 #pragma unroll
@@ -271,14 +278,14 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
         p[v][i] = h * g[i] * w[i];
         sums[0] = __builtin_fmaf(p[v][i], z[i], sums[0]);
       }
-      if (gate_kind == WUSH_GATE_ELEMENT) store8(static_cast<Y*>(dgate) + base + col[v], o);
+      if (ELEMENT) store8(static_cast<Y*>(dgate) + base + col[v], o);
     }
     if (!y) {
       if (a.w_pre) __syncthreads();   // slots[0] is read before the next row writes it
-      continue;
+      return;
     }
     block_sums<2>(sums, slots[1]);
-    if (gate_kind == WUSH_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(dgate)[row] = sums[1];
+    if (GATE == WUSH_GATE_TOKEN && dgate && threadIdx.x == 0) static_cast<float*>(dgate)[row] = sums[1];
     // without a norm after the block dY is p itself
     const float mz = a.w_post ? k1 * sums[0] * inv_d : 0.0f;
 #pragma unroll
@@ -291,6 +298,27 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
       store8(dy + base + col[v], p[v]);
     }
     if (!a.w_pre) __syncthreads();   // slots[1] likewise, where one barrier a row is all there is
+  };
+  // two buffers in turn where the registers allow it (rows up to 8192 columns):
+  // the next row is loaded before the sums over the one in hand
+  int64_t row = blockIdx.x;
+  const int64_t step = gridDim.x;
+  if constexpr (VPT == 1) {
+    Row p, q;
+    if (row < a.n) load(p, row);
+    for (; row < a.n; row += step) {
+      if (row + step < a.n) load(q, row + step);
+      process(p, row);
+      if ((row += step) >= a.n) break;
+      if (row + step < a.n) load(p, row + step);
+      process(q, row);
+    }
+  } else {
+    for (; row < a.n; row += step) {
+      Row p;
+      load(p, row);
+      process(p, row);
+    }
   }
   float* out = part + static_cast<int64_t>(blockIdx.x) * 3 * a.d;
 #pragma unroll
@@ -302,25 +330,33 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, int gate_kin
   }
 }
 
-// Adds the workgroups' column sums: 64 columns a workgroup, its 16 waves take
-// every 16th partial and are joined in order.
+// Adds the workgroups' column sums: 64 columns a workgroup.  A wave reads four
+// partials at a time (16 lanes 256 bytes of each), its 16 waves every 64th.
 __global__ __launch_bounds__(1024) void norm_cols_kernel(int d, int parts, const float* __restrict__ part,
                                                          float* __restrict__ dw_pre, float* __restrict__ dw_post,
                                                          float* __restrict__ dgate) {
-  __shared__ float sh[16][64];
+  __shared__ f32x4 sh[16][16];
   float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
   if (!out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (c < d)
-    for (int i = wave; i < parts; i += 16) s += part[(static_cast<int64_t>(i) * 3 + blockIdx.y) * d + c];
-  sh[wave][lane] = s;
-  __syncthreads();
-  if (wave != 0 || c >= d) return;
-  s = 0.0f;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, c = blockIdx.x * 64 + 4 * j;
+  f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < d) {
+#pragma unroll 4
+    for (int i = 4 * wave + (lane >> 4); i < parts; i += 64)
+      s += *reinterpret_cast<const f32x4*>(part + (static_cast<int64_t>(i) * 3 + blockIdx.y) * d + c);
+  }
 #pragma unroll
-  for (int w = 0; w < 16; ++w) s += sh[w][lane];
-  out[c] = s;
+  for (int k = 0; k < 4; ++k) {
+    s[k] += __shfl_xor(s[k], 16, 64);
+    s[k] += __shfl_xor(s[k], 32, 64);
+  }
+  if (lane < 16) sh[wave][j] = s;
+  __syncthreads();
+  if (wave != 0 || lane >= 16 || c >= d) return;
+  s = sh[0][j];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) s += sh[w][j];
+  *reinterpret_cast<f32x4*>(out + c) = s;
 }
 
 constexpr int kMaxD = 24576;
@@ -329,10 +365,9 @@ constexpr int kMaxD = 24576;
 // in flight together, up to the largest workgroup's 16384 columns.
 int fwd_vpt(int d) { return d <= 16384 ? 2 : 4; }
 
-// The backward kernel's: two up to 8192 columns.  Wider rows take more per
-// thread, so that a workgroup of eight waves (twelve past 16384 columns) still
-// leaves each thread 256 (168) registers for the columns' sums.
-int bwd_vpt(int d) { return d <= 8192 ? 2 : d <= 12288 ? 3 : 4; }
+// The backward kernel's: one up to 8192 columns.  Wider rows take more per
+// thread, and so many registers that only twelve waves (of 168) fit beyond 16384.
+int bwd_vpt(int d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
 
 int threads(int d, int vpt) {
   const int per = 8 * vpt * 64;
@@ -461,15 +496,17 @@ extern "C" wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_
       using YT = decltype(y);
       using RT = decltype(r);
       using UT = decltype(u);
-      auto pick = [&](auto channel) {
-        constexpr bool C = decltype(channel)::value;
-        return d <= 8192    ? norm_bwd_kernel<YT, RT, UT, 2, 512, C>
-               : d <= 12288 ? norm_bwd_kernel<YT, RT, UT, 3, 512, C>
-               : d <= 16384 ? norm_bwd_kernel<YT, RT, UT, 4, 512, C>
-                            : norm_bwd_kernel<YT, RT, UT, 4, 768, C>;
+      auto pick = [&](auto gate) {
+        constexpr int G = decltype(gate)::value;
+        return d <= 8192    ? norm_bwd_kernel<YT, RT, UT, 1, 1024, G>
+               : d <= 16384 ? norm_bwd_kernel<YT, RT, UT, 2, 1024, G>
+                            : norm_bwd_kernel<YT, RT, UT, 4, 768, G>;
       };
-      auto k = gate_kind == WUSH_GATE_CHANNEL ? pick(std::true_type()) : pick(std::false_type());
-      hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a, static_cast<int>(gate_kind),
+      using std::integral_constant;
+      auto k = gate_kind == WUSH_GATE_CHANNEL   ? pick(integral_constant<int, WUSH_GATE_CHANNEL>())
+               : gate_kind == WUSH_GATE_ELEMENT ? pick(integral_constant<int, WUSH_GATE_ELEMENT>())
+                                                : pick(integral_constant<int, WUSH_GATE_TOKEN>());
+      hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a,
                          static_cast<const UT*>(dU), static_cast<const RT*>(dRout), static_cast<const YT*>(Y),
                          static_cast<const RT*>(Rout), static_cast<YT*>(dY), static_cast<RT*>(dR), dgate, part);
       return launched(who);
