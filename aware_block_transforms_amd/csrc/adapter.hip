@@ -233,7 +233,190 @@ struct YRow<bf16_t> {
   }
 };
 
-template <class Y, int RT, int TT>
+// What a spread workgroup knows of its tile.
+struct SpreadTile {
+  int begin, rows, rank, col_wg;
+  int c0, stride;   // the wave's first columns, and the step to its next ones
+};
+
+// Operands of one 16-token tile and 32 ranks: three terms.  At rank 16 the
+// upper half of k is free, and the first two terms share one operand (against
+// the factor's rows twice).
+template <int RT, int TT>
+using SpreadOps = u32x4[TT][(RT + 1) / 2][RT == 1 ? 2 : 3][64];
+
+__device__ __forceinline__ void add8(float* v, const raw8<float>& r) {
+  float w[8];
+  widen8(r, w);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) v[x] += w[x];
+}
+
+// Adds up the parts of V for the tile's tokens and puts its operands into LDS.
+template <int RT, int TT>
+__device__ __forceinline__ void stage_v(const SpreadTile& t, int n, const float* __restrict__ part, int splits,
+                                        float* __restrict__ V, SpreadOps<RT, TT>& vop) {
+  constexpr int R = 16 * RT;
+  const int tiles = (t.rows + 15) / 16;
+  const int64_t v_step = static_cast<int64_t>(n) * R;
+  for (int q = threadIdx.x; q < tiles * 16 * (R / 8); q += 64 * kWaves) {
+    const int row = q / (R / 8), r8 = q % (R / 8);
+    float v[8] = {};
+    if (row < t.rows) {
+      const int64_t at = (static_cast<int64_t>(t.begin) + row) * R + 8 * r8;
+      raw8<float> r;
+      load8(r, part + at);
+      widen8(r, v);
+      int i = 1;
+      for (; i + 3 < splits; i += 4) {   // four loads in flight
+        raw8<float> o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load8(o[k], part + at + (i + k) * v_step);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add8(v, o[k]);
+      }
+      for (; i < splits; ++i) {
+        load8(r, part + at + i * v_step);
+        add8(v, r);
+      }
+      // V itself, where the caller keeps it
+      if (V && t.col_wg == 0) store8(V + at, v);
+    }
+    u32x4 o[3];
+    split8(v, o);
+    u32x4(*to)[64] = vop[row / 16][r8 / 4];
+    const int at = 16 * (r8 & 3) + (row & 15);
+    if constexpr (RT == 1) {
+      to[0][at] = o[0];
+      to[0][at + 32] = o[1];
+      to[1][at] = o[2];
+      to[1][at + 32] = u32x4{0u, 0u, 0u, 0u};
+    } else {
+#pragma unroll
+      for (int m = 0; m < 3; ++m) to[m][at] = o[m];
+    }
+  }
+}
+
+// A wave's columns for KS operands of 32 ranks (0: no adapter, Y = Y0).  Y0 and
+// Y are reached through buffer resources of the tile's rows, whose range check
+// makes zeros of loads, and nothing of stores, past the last row; lanes past the
+// last column use an offset outside.  So no branch stands between a load ahead
+// and its use, and every wait covers only what it is for.
+template <class Y, int RT, int TT, int KS, bool BASE>
+__device__ __forceinline__ void spread_columns(const SpreadTile& t, int n, int d, const float* __restrict__ part,
+                                               int splits, const bf16_t* __restrict__ factor, const Y* y0,
+                                               int64_t ld0, Y* y, int64_t ldy, float* __restrict__ V,
+                                               SpreadOps<RT, TT>& vop) {
+  constexpr int CW = YRow<Y>::CW, TERMS = RT == 1 ? 2 : 3, F = KS > 0 ? KS : 1, B = sizeof(Y);
+  constexpr uint32_t kOutside = 0x80000000u;
+  // the factor rows of the next columns too, where the registers hold both
+  constexpr bool kAhead = TT == 1 && KS * CW <= 16;
+  using raw = typename YRow<Y>::raw;
+  using factors = typename YRow<Y>::factors;
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int tiles = TT == 1 ? 1 : (t.rows + 15) / 16;
+  auto resource = [&](const Y* p, int64_t ld) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<Y*>(p + t.begin * ld), static_cast<short>(0),
+        static_cast<int>(((t.rows - 1) * static_cast<int>(ld) + d) * B), 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t to = resource(y, ldy);
+  const __amdgpu_buffer_rsrc_t base = resource(BASE ? y0 : y, BASE ? ld0 : ldy);
+  factors fr[F][8];
+  auto load_factor = [&](int c0) {
+    const int c = min(c0 + CW * j, d - CW);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
+        fr[ks][i] = *reinterpret_cast<const factors*>(factor + static_cast<int64_t>(min(r, t.rank - 1)) * d + c);
+      }
+  };
+  // the lane's byte offset in a row; opaque, since the compiler would make a
+  // branch of every access out of the choice
+  auto place = [&](int c0) {
+    uint32_t p = c0 + CW * j < d ? static_cast<uint32_t>((c0 + CW * j) * B) : kOutside;
+    asm("" : "+v"(p));
+    return p;
+  };
+  auto row = [&](int i, int e, int64_t ld) { return static_cast<uint32_t>((16 * i + 4 * g + e) * static_cast<int>(ld) * B); };
+  raw in[4];
+  auto load_rows = [&](int i, uint32_t at) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      in[e] = BASE ? __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(base, row(i, e, ld0) + at, 0, 0))
+                   : raw{0, 0, 0, 0};
+  };
+  int c0 = t.c0;
+  load_factor(c0);
+  uint32_t at = place(c0);
+  load_rows(0, at);
+  if (KS > 0 || V) stage_v<RT, TT>(t, n, part, splits, V, vop);
+  if (KS > 0) __syncthreads();
+  if (c0 >= d) return;
+  // everything so far has come (s_waitcnt vmcnt(0)): otherwise the loop's first
+  // wait, which all its turns share, would also cover the stores of the turn
+  // before
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  do {
+    if constexpr (TT == 1 && !kAhead) {
+      if (c0 != t.c0) load_factor(c0);
+    }
+    u32x4 w[F][CW];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
+#pragma unroll
+        for (int q = 0; q < CW / 2; ++q)
+          if (r >= t.rank) fr[ks][i][q] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < CW; ++i)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          w[ks][i][p] = __builtin_amdgcn_perm(fr[ks][2 * p + 1][i / 2], fr[ks][2 * p][i / 2],
+                                              i & 1 ? 0x07060302u : 0x05040100u);
+    }
+    const uint32_t now = at;
+    if constexpr (TT == 1) {
+      c0 += t.stride;
+      at = place(c0);
+      if constexpr (kAhead) load_factor(c0);
+    }
+    for (int i = 0; i < tiles; ++i) {
+      f32x4 acc[CW];
+      YRow<Y> b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e].v = in[e];
+#pragma unroll
+      for (int q = 0; q < CW; ++q) acc[q] = f32x4{b[0].at(q), b[1].at(q), b[2].at(q), b[3].at(q)};
+      load_rows(TT == 1 ? 0 : i + 1, at);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int m = 0; m < TERMS; ++m) {
+          const u32x4 v = vop[i][ks][m][lane];
+#pragma unroll
+          for (int q = 0; q < CW; ++q) acc[q] = mfma(v, w[ks][q], acc[q]);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float s[CW];
+#pragma unroll
+        for (int q = 0; q < CW; ++q) s[q] = acc[q][e];
+        YRow<Y> o;
+        o.put(s);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o.v), to, row(i, e, ldy) + now, 0, 0);
+      }
+    }
+  } while (TT == 1 && c0 < d);
+}
+
+template <class Y, int RT, int TT, bool BASE>
 __global__ __launch_bounds__(64 * kWaves) void adapter_spread_kernel(int n, int d, int col_wgs,
                                                                      const float* __restrict__ part, int splits,
                                                                      int nseg, const int* __restrict__ off,
@@ -243,147 +426,23 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_spread_kernel(int n, int 
                                                                      int64_t ld0, Y* y, int64_t ldy,
                                                                      float* __restrict__ V) {
   constexpr int R = 16 * RT, T = 16 * TT, KS = (R + 31) / 32, CW = YRow<Y>::CW;
-  // Operands of one 16-token tile and 32 ranks: three terms.  At rank 16 the
-  // upper half of k is free, and the first two terms share one operand (against
-  // the factor's rows twice).
-  constexpr int TERMS = RT == 1 ? 2 : 3;
-  using raw = typename YRow<Y>::raw;
-  using factors = typename YRow<Y>::factors;
-  __shared__ u32x4 vop[TT][KS][TERMS][64];
+  __shared__ SpreadOps<RT, TT> vop;
   const int col_wg = blockIdx.x % col_wgs;
   const Tile t = find_tile<T>(blockIdx.x / col_wgs, n, nseg, off, ids, nad);
   if (t.begin >= t.end) return;
-  const int rows = t.end - t.begin, tiles = (rows + 15) / 16;
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // lanes past the last column repeat it and store nothing: the matrix
-  // instructions take their token rows from every lane
-  int c0 = (col_wg * kWaves + wave) * 16 * CW, c = min(c0 + CW * j, d - CW);
   const int rk = t.adapter < 0 ? 0 : min(max(rank[t.adapter], 0), R);
-  raw in[4];
-  auto load_rows = [&](int i) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t row = min(t.begin + 16 * i + 4 * g + e, t.end - 1);
-      in[e] = y0 ? *reinterpret_cast<const raw*>(y0 + row * ld0 + c) : raw{0, 0, 0, 0};
-    }
-  };
-  factors fr[KS][8];
-  auto load_factor = [&]() {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      if (32 * ks >= rk) break;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
-        fr[ks][i] = *reinterpret_cast<const factors*>(
-            factor + (static_cast<int64_t>(t.adapter) * R + min(r, rk - 1)) * d + c);
-      }
-    }
-  };
-  load_rows(0);
-  load_factor();
-  if (rk > 0 || V) {
-    const int64_t v_step = static_cast<int64_t>(n) * R;
-    for (int q = threadIdx.x; q < tiles * 16 * (R / 8); q += 64 * kWaves) {
-      const int row = q / (R / 8), r8 = q % (R / 8);
-      float v[8] = {};
-      if (row < rows) {
-        const float* p = part + (static_cast<int64_t>(t.begin) + row) * R + 8 * r8;
-        raw8<float> r;
-        load8(r, p);
-        widen8(r, v);
-#pragma unroll 4
-        for (int i = 1; i < splits; ++i) {
-          float o[8];
-          load8(r, p + i * v_step);
-          widen8(r, o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] += o[k];
-        }
-        // V itself, where the caller keeps it
-        if (V && col_wg == 0) store8(V + (static_cast<int64_t>(t.begin) + row) * R + 8 * r8, v);
-      }
-      u32x4 o[3];
-      split8(v, o);
-      u32x4(*to)[64] = vop[row / 16][r8 / 4];
-      const int at = 16 * (r8 & 3) + (row & 15);
-      if constexpr (RT == 1) {
-        to[0][at] = o[0];
-        to[0][at + 32] = o[1];
-        to[1][at] = o[2];
-        to[1][at + 32] = u32x4{0u, 0u, 0u, 0u};
-      } else {
-#pragma unroll
-        for (int m = 0; m < 3; ++m) to[m][at] = o[m];
-      }
-    }
-    __syncthreads();
-  }
-  if (c0 >= d) return;
-  const int stride = col_wgs * kWaves * 16 * CW;
-  // the factor rows of the next columns too, where the registers hold both
-  constexpr bool kAhead = TT == 1 && KS * CW <= 16;
-  for (bool again = false;; again = true) {
-    if (TT == 1 && !kAhead && again) load_factor();
-    u32x4 w[KS][CW];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      if (32 * ks >= rk) break;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = RT == 1 ? 8 * (g & 1) + i : 32 * ks + 8 * g + i;
-#pragma unroll
-        for (int q = 0; q < CW / 2; ++q)
-          if (r >= rk) fr[ks][i][q] = 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < CW; ++i)
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          w[ks][i][p] = __builtin_amdgcn_perm(fr[ks][2 * p + 1][i / 2], fr[ks][2 * p][i / 2],
-                                              i & 1 ? 0x07060302u : 0x05040100u);
-    }
-    const int c_now = c;
-    const bool in_c = c0 + CW * j < d, more = TT == 1 && c0 + stride < d;
-    for (int i = 0; i < tiles; ++i) {
-      f32x4 acc[CW];
-      YRow<Y> b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b[e].v = in[e];
-#pragma unroll
-      for (int q = 0; q < CW; ++q) acc[q] = f32x4{b[0].at(q), b[1].at(q), b[2].at(q), b[3].at(q)};
-      if (i + 1 < tiles) {
-        load_rows(i + 1);
-      } else if (more) {
-        c0 += stride;
-        c = min(c0 + CW * j, d - CW);
-        if constexpr (kAhead) load_factor();
-        load_rows(0);
-      }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (32 * ks >= rk) break;
-#pragma unroll
-        for (int m = 0; m < TERMS; ++m) {
-          const u32x4 v = vop[i][ks][m][lane];
-#pragma unroll
-          for (int q = 0; q < CW; ++q) acc[q] = mfma(v, w[ks][q], acc[q]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = t.begin + 16 * i + 4 * g + e;
-        float s[CW];
-#pragma unroll
-        for (int q = 0; q < CW; ++q) s[q] = acc[q][e];
-        YRow<Y> o;
-        o.put(s);
-        if (in_c && row < t.end) *reinterpret_cast<raw*>(y + row * ldy + c_now) = o.v;
-      }
-    }
-    if (!more) break;
-  }
+  const SpreadTile st{t.begin, t.end - t.begin, rk, col_wg, (col_wg * kWaves + wave) * 16 * CW,
+                      col_wgs * kWaves * 16 * CW};
+  const bf16_t* f = factor + static_cast<int64_t>(max(t.adapter, 0)) * R * d;
+  if (rk == 0)
+    spread_columns<Y, RT, TT, 0, BASE>(st, n, d, part, splits, f, y0, ld0, y, ldy, V, vop);
+  else if (KS > 2 && rk > 64)
+    spread_columns<Y, RT, TT, KS, BASE>(st, n, d, part, splits, f, y0, ld0, y, ldy, V, vop);
+  else if (KS > 1 && rk > 32)
+    spread_columns<Y, RT, TT, (KS > 2 ? 2 : KS), BASE>(st, n, d, part, splits, f, y0, ld0, y, ldy, V, vop);
+  else
+    spread_columns<Y, RT, TT, 1, BASE>(st, n, d, part, splits, f, y0, ld0, y, ldy, V, vop);
 }
 
 // V = the sum of the low kernel's parts, where no spread kernel writes it.
@@ -415,7 +474,7 @@ bool short_requests(int n, int nseg) { return n / nseg <= 16; }
 int low_splits(int n, int d, int nseg, int rmax) {
   const int64_t tiles = tile_numbers(n, 16 * low_tiles(n, nseg, rmax), nseg);
   const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves);
-  int s = static_cast<int>((1024 + tiles - 1) / tiles);
+  int s = static_cast<int>(768 / tiles);
   if (s > 16) s = 16;
   if (s > pieces) s = pieces;
   return s < 1 ? 1 : s;
@@ -453,7 +512,8 @@ void spread_by_tiles(bool one, int n, int d, const float* part, int splits, int 
   const int all = (d + cols - 1) / cols, few = tiles < 1024 ? static_cast<int>(1024 / tiles) : 1;
   const int col_wgs = one && few < all ? few : all;
   const dim3 grid(static_cast<unsigned>(col_wgs * tiles));
-  auto k = one ? adapter_spread_kernel<Y, RT, 1> : adapter_spread_kernel<Y, RT, 4>;
+  auto k = one ? (y0 ? adapter_spread_kernel<Y, RT, 1, true> : adapter_spread_kernel<Y, RT, 1, false>)
+               : (y0 ? adapter_spread_kernel<Y, RT, 4, true> : adapter_spread_kernel<Y, RT, 4, false>);
   hipLaunchKernelGGL(k, grid, dim3(64 * kWaves), 0, s, n, d, col_wgs, part, splits, nseg, off, ids, nad,
                      static_cast<const bf16_t*>(factor), rank, static_cast<const Y*>(y0), ld0, static_cast<Y*>(y), ldy,
                      V);
@@ -478,6 +538,9 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kMaxSeg = 1 << 20;
 constexpr int kMaxTokens = 1 << 24;   // so that sums over 64 requests stay in 32 bits
+// Row strides of Y and Y0: the 64 rows of a workgroup stay below 2^31 bytes.
+constexpr int64_t kMaxStride = 1 << 22;
+
 // X as the grad kernel sees it: the two float types and the act8 codes.
 constexpr int kAct8 = 2;
 
@@ -519,6 +582,8 @@ extern "C" wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int 
   if (st != WUSH_OK) return st;
   if (ldx < d_in || ldx % 8 || ldy < d_out || ldy % 8 || (Y0 && (ldy0 < d_out || ldy0 % 8)))
     return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
+  if (ldy > kMaxStride || (Y0 && ldy0 > kMaxStride))
+    return fail(WUSH_E_SHAPE, "%s: rows of Y above %lld values", who, static_cast<long long>(kMaxStride));
   if (n == 0) return WUSH_OK;
   if (!X || !seg_off || !seg_adapter || !A || !Bt || !rank || !alpha || !Y) return fail(WUSH_E_ARG, "%s: null pointer", who);
   for (const void* p : {X, A, Bt, Y0, static_cast<const void*>(Y), static_cast<const void*>(V), static_cast<const void*>(ws)})
@@ -564,6 +629,8 @@ extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wus
   if (ldg < d_out || ldg % 8 || ldx < d_in || ldx % 8 || (dX && (lddx < d_in || lddx % 8)) ||
       (dX && dX0 && (lddx0 < d_in || lddx0 % 8)))
     return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
+  if (dX && (lddx > kMaxStride || (dX0 && lddx0 > kMaxStride)))
+    return fail(WUSH_E_SHAPE, "%s: rows of dX above %lld values", who, static_cast<long long>(kMaxStride));
   if (!adapter_grads_fit(n, d_in, d_out, nad, rmax)) return fail(WUSH_E_SHAPE, "%s: nad=%d passes the launch limit", who, nad);
   if (x_scales && (d_in % 32 || ldx != d_in))
     return fail(WUSH_E_SHAPE, "%s: an act8 checkpoint has whole groups of 32 and no row stride of its own", who);
