@@ -10,10 +10,14 @@
 // rounding.  A group with a NaN or an infinity gets byte 0xFF and zero codes
 // and reads back as NaN, as the other formats' blocks do.
 //
-// All four kernels move bytes and do little else.  A lane owns eight values, a
-// group is four neighbouring lanes (its maximum takes two DPP steps), and a
-// wave one 512-value piece of a row, so that rows of any length lose at most
-// part of one wave.
+// All four kernels move bytes and do little else.  A wave owns a 512-value piece
+// of a row, so that rows of any length lose at most part of one wave.  A lane
+// holds eight of its values: eight neighbours where everything is bf16 (16 bytes
+// an access), two runs of four where something is fp32, so that each access of
+// the wave covers whole lines either way; a group is then four or eight
+// neighbouring lanes, and its maximum takes two or three DPP steps.  Results
+// that a later pass reads are written past the caches where they are larger
+// than those (non-temporal stores).
 
 #include <hip/hip_runtime.h>
 
@@ -29,39 +33,93 @@ namespace {
 constexpr int kWaves = 4;   // per workgroup
 
 template <int CTRL>
-__device__ __forceinline__ uint32_t quad(uint32_t v) {
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return __builtin_amdgcn_update_dpp(0u, v, CTRL, 0xf, 0xf, true);
 }
 
+// N neighbouring values of a row, as fp32.
+template <class T, int N>
+struct Run;
+template <>
+struct Run<float, 4> {
+  f32x4 r;
+  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
+  __device__ __forceinline__ void widen(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = r[i];
+  }
+};
+template <>
+struct Run<bf16_t, 4> {
+  u32x2 r;
+  __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const u32x2*>(p); }
+  __device__ __forceinline__ void widen(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __builtin_bit_cast(float, i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+  }
+};
+template <>
+struct Run<bf16_t, 8> {
+  raw8<bf16_t> r;
+  __device__ __forceinline__ void load(const bf16_t* p) { load8(r, p); }
+  __device__ __forceinline__ void widen(float* v) const { widen8(r, v); }
+};
+
+template <bool PAST, class V>
+__device__ __forceinline__ void put(V v, V* p) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
+template <bool PAST, int N>
+__device__ __forceinline__ void put_run(float* p, const float* v) {
+  static_assert(N == 4, "fp32 runs are 16 bytes");
+  put<PAST>(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+}
+template <bool PAST, int N>
+__device__ __forceinline__ void put_run(bf16_t* p, const float* v) {
+  if constexpr (N == 4)
+    put<PAST>(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, reinterpret_cast<u32x2*>(p));
+  else
+    put<PAST>(u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])},
+              reinterpret_cast<u32x4*>(p));
+}
+
+template <int N>
 struct Codes {
-  u32x2 q;
+  uint32_t q[N / 4];
   uint32_t byte;
 };
 
-// Codes of the lane's eight values and the group's scale byte.
-__device__ __forceinline__ Codes encode(const float* v) {
+// Codes of the lane's N values and its group's scale byte.
+template <int N>
+__device__ __forceinline__ Codes<N> encode(const float* v) {
   // |x| as bits: integer order is the order of magnitudes, and NaN and
   // infinities are those from 0x7f800000 on
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
-  a = max(a, quad<0xB1>(a));   // lanes 1 0 3 2
-  a = max(a, quad<0x4E>(a));   // lanes 2 3 0 1
+  for (int i = 0; i < N; ++i) a = max(a, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+  a = max(a, dpp<0xB1>(a));    // lanes 1 0 3 2
+  a = max(a, dpp<0x4E>(a));    // lanes 2 3 0 1
+  if constexpr (N == 4) a = max(a, dpp<0x141>(a));   // lanes 7 6 5 4 3 2 1 0
   const bool bad = a >= 0x7f800000u;
   const uint32_t byte = max(a >> 23, 7u);   // e + 127
   const float m = __builtin_bit_cast(float, (260u - byte) << 23);   // 2^(6-e)
   // adding 1.5 * 2^23 rounds to the nearest integer (ties to even) and leaves
   // its two's complement in the low bits; x m is exact inside the fma
   constexpr float kRound = 12582912.0f;
-  uint32_t b[8];
+  uint32_t b[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float r = __builtin_fmaf(v[i], m, kRound);
     b[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(r, kRound - 127.0f, kRound + 127.0f));
   }
-  Codes c;
+  Codes<N> c;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < N / 4; ++h) {
     const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
     const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000c0cu);
     c.q[h] = bad ? 0u : lo | hi;
@@ -70,64 +128,99 @@ __device__ __forceinline__ Codes encode(const float* v) {
   return c;
 }
 
-__device__ __forceinline__ void decode(u32x2 q, uint32_t byte, float* v) {
+template <int N>
+__device__ __forceinline__ void decode(const Codes<N>& c, float* v) {
   // 2^(e-6); bytes below 7 do not occur in a checkpoint and read as zero
-  const uint32_t s = byte == 255u ? 0x7fc00000u : (max(byte, 6u) - 6u) << 23;
+  const uint32_t s = c.byte == 255u ? 0x7fc00000u : (max(c.byte, 6u) - 6u) << 23;
   const float m = __builtin_bit_cast(float, s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(static_cast<int8_t>(q[i / 4] >> (8 * (i & 3)))) * m;
+  for (int i = 0; i < N; ++i) v[i] = static_cast<float>(static_cast<int8_t>(c.q[i / 4] >> (8 * (i & 3)))) * m;
 }
 
-// The wave's row and the lane's first column; false past the end.
+// The wave's row and the lane's runs of N columns; a run may lie past the end.
+template <int N>
 struct Place {
+  static constexpr int kRuns = 8 / N;
   int64_t row;
-  int col;
+  int col[kRuns];
+  bool in[kRuns];
 };
-__device__ __forceinline__ bool place(int64_t n, int d, int per_row, Place& p) {
+template <int N>
+__device__ __forceinline__ Place<N> place(int64_t n, int d, int per_row) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t piece = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
+  Place<N> p;
   p.row = piece / per_row;
-  p.col = static_cast<int>(piece - p.row * per_row) * 512 + (threadIdx.x & 63) * 8;
-  return p.row < n && p.col < d;
+#pragma unroll
+  for (int r = 0; r < Place<N>::kRuns; ++r) {
+    p.col[r] = static_cast<int>(piece - p.row * per_row) * 512 + r * 64 * N + (threadIdx.x & 63) * N;
+    p.in[r] = p.row < n && p.col[r] < d;
+  }
+  return p;
 }
 
-__device__ __forceinline__ void put_codes(const Codes& c, const Place& p, int d, uint8_t* codes, uint8_t* scales) {
-  *reinterpret_cast<u32x2*>(codes + p.row * d + p.col) = c.q;
-  if ((threadIdx.x & 3) == 0) scales[p.row * (d / 32) + p.col / 32] = static_cast<uint8_t>(c.byte);
+template <int N>
+__device__ __forceinline__ void put_codes(const Codes<N>& c, int64_t row, int col, int d, uint8_t* codes,
+                                          uint8_t* scales) {
+  if constexpr (N == 4)
+    *reinterpret_cast<uint32_t*>(codes + row * d + col) = c.q[0];
+  else
+    *reinterpret_cast<u32x2*>(codes + row * d + col) = u32x2{c.q[0], c.q[1]};
+  if ((threadIdx.x & (32 / N - 1)) == 0) scales[row * (d / 32) + col / 32] = static_cast<uint8_t>(c.byte);
 }
 
-__device__ __forceinline__ void get_codes(const Place& p, int d, const uint8_t* codes, const uint8_t* scales, u32x2& q,
-                                          uint32_t& byte) {
-  q = *reinterpret_cast<const u32x2*>(codes + p.row * d + p.col);
-  byte = scales[p.row * (d / 32) + p.col / 32];
+template <int N>
+__device__ __forceinline__ void get_codes(int64_t row, int col, int d, const uint8_t* codes, const uint8_t* scales,
+                                          Codes<N>& c) {
+  if constexpr (N == 4) {
+    c.q[0] = *reinterpret_cast<const uint32_t*>(codes + row * d + col);
+  } else {
+    const u32x2 q = *reinterpret_cast<const u32x2*>(codes + row * d + col);
+    c.q[0] = q[0];
+    c.q[1] = q[1];
+  }
+  c.byte = scales[row * (d / 32) + col / 32];
 }
 
-template <class T>
+// Values per run: see the top.
+template <class A, class B>
+constexpr int run_of = is_f32<A> || is_f32<B> ? 4 : 8;
+
+template <class T, int N = run_of<T, T>>
 __global__ __launch_bounds__(64 * kWaves) void act8_pack_kernel(int64_t n, int d, int per_row, const T* __restrict__ X,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
-  Place p;
-  if (!place(n, d, per_row, p)) return;
-  raw8<T> r;
-  load8(r, X + p.row * d + p.col);
-  float v[8];
-  widen8(r, v);
-  put_codes(encode(v), p, d, codes, scales);
+  const auto p = place<N>(n, d, per_row);
+  Run<T, N> x[p.kRuns];
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r)
+    if (p.in[r]) x[r].load(X + p.row * d + p.col[r]);
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r) {
+    if (!p.in[r]) continue;
+    float v[N];
+    x[r].widen(v);
+    put_codes<N>(encode<N>(v), p.row, p.col[r], d, codes, scales);
+  }
 }
 
-template <class T>
+template <class T, bool PAST, int N = run_of<T, T>>
 __global__ __launch_bounds__(64 * kWaves) void act8_unpack_kernel(int64_t n, int d, int per_row,
                                                                   const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales,
                                                                   T* __restrict__ Y) {
-  Place p;
-  if (!place(n, d, per_row, p)) return;
-  u32x2 q;
-  uint32_t byte;
-  get_codes(p, d, codes, scales, q, byte);
-  float v[8];
-  decode(q, byte, v);
-  store8(Y + p.row * d + p.col, v);
+  const auto p = place<N>(n, d, per_row);
+  Codes<N> c[p.kRuns];
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r)
+    if (p.in[r]) get_codes<N>(p.row, p.col[r], d, codes, scales, c[r]);
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r) {
+    if (!p.in[r]) continue;
+    float v[N];
+    decode<N>(c[r], v);
+    put_run<PAST, N>(Y + p.row * d + p.col[r], v);
+  }
 }
 
 // 1 / (1 + exp(-x)) on the transcendental unit: 1 to 2 ulp where it matters
@@ -136,58 +229,77 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
 }
 
-template <class T, class H, bool KEEP>
+template <class T, class H, bool KEEP, bool PAST, int N = run_of<T, H>>
 __global__ __launch_bounds__(64 * kWaves) void act8_swiglu_kernel(int64_t n, int d, int per_row,
                                                                   const T* __restrict__ G, const T* __restrict__ U,
                                                                   int64_t ld, H* __restrict__ out,
                                                                   uint8_t* __restrict__ gc, uint8_t* __restrict__ gs,
                                                                   uint8_t* __restrict__ uc, uint8_t* __restrict__ us) {
-  Place p;
-  if (!place(n, d, per_row, p)) return;
-  raw8<T> rg, ru;
-  load8(rg, G + p.row * ld + p.col);
-  load8(ru, U + p.row * ld + p.col);
-  float g[8], u[8], h[8];
-  widen8(rg, g);
-  widen8(ru, u);
+  const auto p = place<N>(n, d, per_row);
+  Run<T, N> rg[p.kRuns], ru[p.kRuns];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
-  store8(out + p.row * d + p.col, h);
-  if (KEEP) {
-    put_codes(encode(g), p, d, gc, gs);
-    put_codes(encode(u), p, d, uc, us);
+  for (int r = 0; r < p.kRuns; ++r)
+    if (p.in[r]) {
+      rg[r].load(G + p.row * ld + p.col[r]);
+      ru[r].load(U + p.row * ld + p.col[r]);
+    }
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r) {
+    if (!p.in[r]) continue;
+    float g[N], u[N], h[N];
+    rg[r].widen(g);
+    ru[r].widen(u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
+    put_run<PAST, N>(out + p.row * d + p.col[r], h);
+    if (KEEP) {
+      put_codes<N>(encode<N>(g), p.row, p.col[r], d, gc, gs);
+      put_codes<N>(encode<N>(u), p.row, p.col[r], d, uc, us);
+    }
   }
 }
 
 // With s = sigmoid(g): dU = dH g s, dG = dH u s (1 + g (1 - s)).
-template <class H, class T>
+template <class H, class T, bool PAST, int N = run_of<T, H>>
 __global__ __launch_bounds__(64 * kWaves) void act8_swiglu_bwd_kernel(
     int64_t n, int d, int per_row, const H* __restrict__ dH, const uint8_t* __restrict__ gc,
     const uint8_t* __restrict__ gs, const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
     T* __restrict__ dG, T* __restrict__ dU, int64_t ld) {
-  Place p;
-  if (!place(n, d, per_row, p)) return;
-  raw8<H> rh;
-  u32x2 qg, qu;
-  uint32_t bg, bu;
-  load8(rh, dH + p.row * d + p.col);
-  get_codes(p, d, gc, gs, qg, bg);
-  get_codes(p, d, uc, us, qu, bu);
-  float dh[8], g[8], u[8];
-  widen8(rh, dh);
-  decode(qg, bg, g);
-  decode(qu, bu, u);
+  const auto p = place<N>(n, d, per_row);
+  Run<H, N> rh[p.kRuns];
+  Codes<N> cg[p.kRuns], cu[p.kRuns];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = sigmoid(g[i]), hs = dh[i] * s;
-    u[i] = hs * u[i] * __builtin_fmaf(g[i], 1.0f - s, 1.0f);
-    g[i] = hs * g[i];
+  for (int r = 0; r < p.kRuns; ++r)
+    if (p.in[r]) {
+      rh[r].load(dH + p.row * d + p.col[r]);
+      get_codes<N>(p.row, p.col[r], d, gc, gs, cg[r]);
+      get_codes<N>(p.row, p.col[r], d, uc, us, cu[r]);
+    }
+#pragma unroll
+  for (int r = 0; r < p.kRuns; ++r) {
+    if (!p.in[r]) continue;
+    float dh[N], g[N], u[N];
+    rh[r].widen(dh);
+    decode<N>(cg[r], g);
+    decode<N>(cu[r], u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = sigmoid(g[i]), hs = dh[i] * s;
+      u[i] = hs * u[i] * __builtin_fmaf(g[i], 1.0f - s, 1.0f);
+      g[i] = hs * g[i];
+    }
+    put_run<PAST, N>(dG + p.row * ld + p.col[r], u);
+    put_run<PAST, N>(dU + p.row * ld + p.col[r], g);
   }
-  store8(dG + p.row * ld + p.col, u);
-  store8(dU + p.row * ld + p.col, g);
 }
 
 int per_row(int d) { return (d + 511) / 512; }
+
+// Whether an output of n x d values passes the 256 MB of the last-level cache:
+// then it is written past the caches, which keeps them for the inputs.
+bool past(int n, int d, wush_dtype t) {
+  return static_cast<int64_t>(n) * d * (t == WUSH_F32 ? 4 : 2) > (int64_t{256} << 20);
+}
 
 // Workgroups of n rows, 0 if they pass the launch limit.
 unsigned blocks(int n, int d) {
@@ -237,10 +349,11 @@ extern "C" wush_status wush_act8_unpack(wush_dtype ydt, int n, int d, const int8
   hipStream_t s = static_cast<hipStream_t>(stream);
   const uint8_t* c = reinterpret_cast<const uint8_t*>(codes);
   const dim3 grid(blocks(n, d)), wg(64 * kWaves);
+  const bool far = past(n, d, ydt);
   if (ydt == WUSH_F32)
-    hipLaunchKernelGGL(act8_unpack_kernel<float>, grid, wg, 0, s, n, d, per_row(d), c, scales, static_cast<float*>(Y));
+    hipLaunchKernelGGL((far ? act8_unpack_kernel<float, true> : act8_unpack_kernel<float, false>), grid, wg, 0, s, n, d, per_row(d), c, scales, static_cast<float*>(Y));
   else
-    hipLaunchKernelGGL(act8_unpack_kernel<bf16_t>, grid, wg, 0, s, n, d, per_row(d), c, scales, static_cast<bf16_t*>(Y));
+    hipLaunchKernelGGL((far ? act8_unpack_kernel<bf16_t, true> : act8_unpack_kernel<bf16_t, false>), grid, wg, 0, s, n, d, per_row(d), c, scales, static_cast<bf16_t*>(Y));
   return launched("wush_act8_unpack");
 }
 
@@ -250,7 +363,9 @@ template <class T, class H>
 void swiglu(bool keep, int n, int d, const void* G, const void* U, int64_t ld, void* out, uint8_t* gc, uint8_t* gs,
             uint8_t* uc, uint8_t* us, hipStream_t s) {
   const dim3 grid(blocks(n, d)), wg(64 * kWaves);
-  auto k = keep ? act8_swiglu_kernel<T, H, true> : act8_swiglu_kernel<T, H, false>;
+  const bool far = past(n, d, is_f32<H> ? WUSH_F32 : WUSH_BF16);
+  auto k = keep ? (far ? act8_swiglu_kernel<T, H, true, true> : act8_swiglu_kernel<T, H, true, false>)
+                : (far ? act8_swiglu_kernel<T, H, false, true> : act8_swiglu_kernel<T, H, false, false>);
   hipLaunchKernelGGL(k, grid, wg, 0, s, n, d, per_row(d), static_cast<const T*>(G), static_cast<const T*>(U), ld,
                      static_cast<H*>(out), gc, gs, uc, us);
 }
@@ -259,7 +374,8 @@ template <class H, class T>
 void swiglu_bwd(int n, int d, const void* dH, const uint8_t* gc, const uint8_t* gs, const uint8_t* uc,
                 const uint8_t* us, void* dG, void* dU, int64_t ld, hipStream_t s) {
   const dim3 grid(blocks(n, d)), wg(64 * kWaves);
-  hipLaunchKernelGGL((act8_swiglu_bwd_kernel<H, T>), grid, wg, 0, s, n, d, per_row(d), static_cast<const H*>(dH), gc,
+  const bool far = past(n, d, is_f32<T> ? WUSH_F32 : WUSH_BF16);
+  hipLaunchKernelGGL((far ? act8_swiglu_bwd_kernel<H, T, true> : act8_swiglu_bwd_kernel<H, T, false>), grid, wg, 0, s, n, d, per_row(d), static_cast<const H*>(dH), gc,
                      gs, uc, us, static_cast<T*>(dG), static_cast<T*>(dU), ld);
 }
 
