@@ -155,12 +155,149 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
   }
 }
 
-// Partial column sums of one workgroup: [3][d] (dw_pre, dw_post, dgate).  A row
-// stays in registers as it lies in memory and is widened where it is used, so
-// that the columns' sums fit beside it.  MAXT: the largest workgroup, which
-// sets the registers a thread may have.
+// Partial column sums of one workgroup: [3][d] (dw_pre, dw_post, dgate).  A
+// thread owns eight columns of rows up to 8 MAXT.  The next row is loaded, into
+// a second buffer, before the sums over the one in hand.  Loads return in order,
+// so nothing may be loaded and waited for in between: the weights lie in LDS
+// (zero past the last column, which also drops what the threads there add to a
+// sum; they read the last columns again), the two rsqrt values come through the
+// scalar cache, and tensors that the caller left out are read as one that is
+// there and replaced by zeros, not skipped by a branch.
+template <class Y, class R, class U, int MAXT, int GATE>
+__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float* __restrict__ k1s,
+                                                        const float* __restrict__ k2s, const U* __restrict__ du,
+                                                        const R* drout, bool has_drout, const Y* __restrict__ y,
+                                                        bool has_y, const R* __restrict__ rout, Y* __restrict__ dy,
+                                                        R* dr, void* __restrict__ dgate, float* __restrict__ part) {
+  constexpr bool CHANNEL = GATE == WUSH_GATE_CHANNEL, ELEMENT = GATE == WUSH_GATE_ELEMENT;
+  __shared__ float slots[2][2 * 16];
+  __shared__ f32x4 weights[CHANNEL ? 3 : 2][MAXT][2];
+  const int me = threadIdx.x, col = min(8 * me, a.d - 8);
+  const bool in = 8 * me < a.d, has_pre = a.w_pre != nullptr, has_post = a.w_post != nullptr;
+  auto keep = [&](int which, const float* from, float otherwise) {
+    f32x4 w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = from ? reinterpret_cast<const f32x4*>(from + col)[h] : f32x4{otherwise, otherwise, otherwise, otherwise};
+      weights[which][me][h] = in ? w[h] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
+  keep(0, a.w_pre, 0.0f);
+  keep(1, a.w_post, 1.0f);
+  if constexpr (CHANNEL) keep(2, static_cast<const float*>(a.gate), 1.0f);
+  // no barrier: a thread reads what it wrote itself
+  auto weight = [&](int which, float* v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 w = weights[which][me][h];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i];
+    }
+  };
+  float s_pre[8], s_post[8], s_gate[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = s_gate[i] = 0.0f;
+  const float inv_d = 1.0f / a.d;
+  struct Row {
+    raw8<U> u;
+    raw8<R> r, d;
+    raw8<Y> y, g;
+  };
+  auto load = [&](Row& to, int64_t row) {
+    const int64_t at = row * a.d + col;
+    load8(to.u, du + at);
+    load8(to.r, rout + at);
+    load8(to.d, drout + at);
+    load8(to.y, y + at);
+    if constexpr (ELEMENT) load8(to.g, static_cast<const Y*>(a.gate) + at);
+  };
+  auto process = [&](const Row& now, int64_t row) {
+    const int64_t at = row * a.d + col;
+    const float k1 = has_post ? k1s[row] : 1.0f, k2 = has_pre ? k2s[row] : 0.0f;
+    float q[8], x[8], w[8], m = 0.0f;
+    widen8(now.u, q);
+    widen8(now.r, x);
+    weight(0, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = has_pre ? x[i] * k2 : 0.0f;
+      q[i] = has_pre ? q[i] : 0.0f;
+      s_pre[i] = __builtin_fmaf(q[i], x[i], s_pre[i]);
+      q[i] *= w[i];
+      m = __builtin_fmaf(q[i], x[i], m);
+    }
+    block_sums<1>(&m, slots[0]);
+    m *= inv_d;
+    float t[8], z[8], g[8], o[8], sums[2] = {0.0f, 0.0f};   // p z, and the token gate's gradient
+    widen8(now.d, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = __builtin_fmaf(k2, __builtin_fmaf(-x[i], m, q[i]), has_drout ? t[i] : 0.0f);
+    if (dr && in) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = a.res * t[i];
+      store8(dr + at, o);
+    }
+    if (!has_y) {
+      __syncthreads();   // slots[0] is read before the next row writes it
+      return;
+    }
+    const float gate_t = GATE == WUSH_GATE_TOKEN && a.gate ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    widen8(now.y, z);
+    weight(1, w);
+    if constexpr (CHANNEL)
+      weight(2, g);
+    else if constexpr (ELEMENT)
+      widen8(now.g, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (!CHANNEL && !ELEMENT) g[i] = gate_t;
+      const float h = a.branch * t[i];
+      z[i] *= k1;
+      const float hz = h * z[i];
+      o[i] = hz * w[i];
+      if (CHANNEL) s_gate[i] += o[i];
+      sums[1] += o[i];
+      s_post[i] = __builtin_fmaf(hz, g[i], s_post[i]);
+      t[i] = h * g[i] * w[i];   // p
+      sums[0] = __builtin_fmaf(t[i], z[i], sums[0]);
+    }
+    if constexpr (ELEMENT)
+      if (in) store8(static_cast<Y*>(dgate) + at, o);
+    block_sums<2>(sums, slots[1]);
+    if (GATE == WUSH_GATE_TOKEN && dgate && me == 0) static_cast<float*>(dgate)[row] = sums[1];
+    // without a norm after the block dY is p itself
+    const float mz = has_post ? sums[0] * inv_d : 0.0f;
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = k1 * __builtin_fmaf(-z[i], mz, t[i]);
+      store8(dy + at, o);
+    }
+  };
+  // two buffers in turn; past the last row the last one is loaded again
+  const int64_t last = a.n - 1, step = gridDim.x;
+  int64_t row = blockIdx.x;
+  Row p, q;
+  load(p, row);
+  for (;;) {
+    load(q, min(row + step, last));
+    process(p, row);
+    if ((row += step) > last) break;
+    load(p, min(row + step, last));
+    process(q, row);
+    if ((row += step) > last) break;
+  }
+  if (!in) return;
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 3 * a.d + col;
+  if (has_pre) store8(out, s_pre);
+  if (has_y && has_post) store8(out + a.d, s_post);
+  if (CHANNEL) store8(out + 2 * a.d, s_gate);
+}
+
+// The same for rows above 8192 columns, VPT pieces a thread.  A row stays in
+// registers as it lies in memory and is widened where it is used; even so the
+// widest spill.
 template <class Y, class R, class U, int VPT, int MAXT, int GATE>
-__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const U* __restrict__ du,
+__global__ __launch_bounds__(MAXT) void norm_bwd_wide_kernel(NormArgs a, const U* __restrict__ du,
                                                         const R* drout, const Y* __restrict__ y,
                                                         const R* __restrict__ rout, Y* __restrict__ dy, R* dr,
                                                         void* __restrict__ dgate, float* __restrict__ part) {
@@ -299,26 +436,10 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const U* __r
     }
     if (!a.w_pre) __syncthreads();   // slots[1] likewise, where one barrier a row is all there is
   };
-  // two buffers in turn where the registers allow it (rows up to 8192 columns):
-  // the next row is loaded before the sums over the one in hand
-  int64_t row = blockIdx.x;
-  const int64_t step = gridDim.x;
-  if constexpr (VPT == 1) {
-    Row p, q;
-    if (row < a.n) load(p, row);
-    for (; row < a.n; row += step) {
-      if (row + step < a.n) load(q, row + step);
-      process(p, row);
-      if ((row += step) >= a.n) break;
-      if (row + step < a.n) load(p, row + step);
-      process(q, row);
-    }
-  } else {
-    for (; row < a.n; row += step) {
-      Row p;
-      load(p, row);
-      process(p, row);
-    }
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    Row p;
+    load(p, row);
+    process(p, row);
   }
   float* out = part + static_cast<int64_t>(blockIdx.x) * 3 * a.d;
 #pragma unroll
@@ -374,14 +495,12 @@ int threads(int d, int vpt) {
   return 64 * ((d + per - 1) / per);
 }
 
-// Workgroups of the backward kernel: about twelve waves for each of the 256
-// compute units, which is what fits, but each with eight rows at least while
-// every unit has one.
+// Workgroups of the backward kernel: sixteen waves for each of the 256 compute
+// units, which is what fits.
 int bwd_groups(int n, int d) {
   const int waves = threads(d, bwd_vpt(d)) / 64;
-  const int fit = 256 * ((12 + waves - 1) / waves), rows = (n + 7) / 8;
-  const int g = rows < fit ? rows : fit;
-  return g >= 256 ? g : n < 256 ? n : 256;
+  const int fit = 256 * (waves > 16 ? 1 : 16 / waves);
+  return n < fit ? n : fit;
 }
 
 wush_status check(const char* who, wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d, wush_gate gate_kind,
@@ -492,23 +611,40 @@ extern "C" wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_
   const int groups = n > 0 ? bwd_groups(n, d) : 0;
   wush_status out = WUSH_OK;
   if (n > 0)
-    out = by_types(ydt, rdt, udt, [&](auto y, auto r, auto u) {
+    out = by_types(Y ? ydt : rdt, rdt, dU ? udt : rdt, [&](auto y, auto r, auto u) {
       using YT = decltype(y);
       using RT = decltype(r);
       using UT = decltype(u);
-      auto pick = [&](auto gate) {
+      const YT* Yp = static_cast<const YT*>(Y);
+      const RT* dRp = static_cast<const RT*>(dRout);
+      const RT* Rp = static_cast<const RT*>(Rout);
+      const UT* dUp = static_cast<const UT*>(dU);
+      auto run = [&](auto gate) {
         constexpr int G = decltype(gate)::value;
-        return d <= 8192    ? norm_bwd_kernel<YT, RT, UT, 1, 1024, G>
-               : d <= 16384 ? norm_bwd_kernel<YT, RT, UT, 2, 1024, G>
-                            : norm_bwd_kernel<YT, RT, UT, 4, 768, G>;
+        if (d > 8192) {
+          auto k = d <= 16384 ? norm_bwd_wide_kernel<YT, RT, UT, 2, 1024, G> : norm_bwd_wide_kernel<YT, RT, UT, 4, 768, G>;
+          hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a, dUp, dRp, Yp, Rp,
+                             static_cast<YT*>(dY), static_cast<RT*>(dR), dgate, part);
+          return;
+        }
+        // stand-ins for what is left out: at least one of dRout and the pair
+        // dU, Rout is there, and no type but Y's may be wider than R's
+        const RT* some = dRp ? dRp : Rp;
+        auto k = d <= 1024   ? norm_bwd_kernel<YT, RT, UT, 128, G>
+                 : d <= 4096 ? norm_bwd_kernel<YT, RT, UT, 512, G>
+                             : norm_bwd_kernel<YT, RT, UT, 1024, G>;
+        hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a, rstd_post, rstd_pre,
+                           dUp ? dUp : reinterpret_cast<const UT*>(some), some, dRp != nullptr,
+                           Yp ? Yp : reinterpret_cast<const YT*>(some), Yp != nullptr, w_pre ? Rp : some,
+                           static_cast<YT*>(dY), static_cast<RT*>(dR), dgate, part);
       };
       using std::integral_constant;
-      auto k = gate_kind == WUSH_GATE_CHANNEL   ? pick(integral_constant<int, WUSH_GATE_CHANNEL>())
-               : gate_kind == WUSH_GATE_ELEMENT ? pick(integral_constant<int, WUSH_GATE_ELEMENT>())
-                                                : pick(integral_constant<int, WUSH_GATE_TOKEN>());
-      hipLaunchKernelGGL(k, dim3(groups), dim3(threads(d, bwd_vpt(d))), 0, s, a,
-                         static_cast<const UT*>(dU), static_cast<const RT*>(dRout), static_cast<const YT*>(Y),
-                         static_cast<const RT*>(Rout), static_cast<YT*>(dY), static_cast<RT*>(dR), dgate, part);
+      if (gate_kind == WUSH_GATE_CHANNEL)
+        run(integral_constant<int, WUSH_GATE_CHANNEL>());
+      else if (gate_kind == WUSH_GATE_ELEMENT)
+        run(integral_constant<int, WUSH_GATE_ELEMENT>());
+      else
+        run(integral_constant<int, WUSH_GATE_TOKEN>());
       return launched(who);
     });
   if (out == WUSH_OK && cols) {
