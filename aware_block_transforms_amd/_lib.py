@@ -424,21 +424,27 @@ def _dt(t, name):
 
 def _want(t, name, shape, dtype=None):
     """A contiguous tensor of that shape (and dtype), or an exception."""
+    if t.shape == shape and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return
     if tuple(t.shape) != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _rows(t, name, n, d):
     """Row stride of an [n][d] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != d:
+    if t.shape != (n, d):
         raise ValueError("%s must have shape (%d, %d), not %s" % (name, n, d, tuple(t.shape)))
-    if t.stride(1) != 1 and d > 1:
+    if n <= 1:
+        if not t.is_contiguous():
+            raise ValueError("%s must have contiguous rows" % name)
+        return d
+    ld, one = t.stride()
+    if one != 1 and d > 1:
         raise ValueError("%s must have contiguous rows" % name)
-    return t.stride(0) if n > 1 else d
+    return ld
 
 
 def _gate(gate, n, d, ydt):
@@ -459,25 +465,36 @@ def wush_block_norm(Y, w_post, gate, R, w_pre, Rout, U, rstd_post=None, rstd_pre
                     eps=1e-6, stream=None):
     """Rout = res_scale R + branch_scale gate norm(Y) w_post; U = norm(Rout) w_pre.  Y, w_post, gate, w_pre with U, and
     Rout may be None; gate is [d], [n][1] (float32) or [n][d] (Y's dtype)."""
-    n, d = R.shape
-    _want(R, "R", (n, d))
+    shape = n, d = R.shape
+    _want(R, "R", shape)
+    rdt = ydt = udt = _dt(R, "R")
+    y = wp = g = ro = wn = u = kp = kn = None
     if Y is not None:
-        _want(Y, "Y", (n, d))
-    if Rout is not None:
-        _want(Rout, "Rout", (n, d), R.dtype)
-    if U is not None:
-        _want(U, "U", (n, d))
-    for t, name, size in ((w_post, "w_post", d), (w_pre, "w_pre", d), (rstd_post, "rstd_post", n),
-                          (rstd_pre, "rstd_pre", n)):
-        if t is not None:
-            _want(t, name, (size,), torch.float32)
+        _want(Y, "Y", shape)
+        ydt, y = _dt(Y, "Y"), Y.data_ptr()
+    if w_post is not None:
+        _want(w_post, "w_post", (d,), torch.float32)
+        wp = w_post.data_ptr()
+    if gate is not None:
+        g = gate.data_ptr()
     kind = _gate(gate, n, d, None if Y is None else Y.dtype)
-    rdt = _dt(R, "R")
-    ydt = rdt if Y is None else _dt(Y, "Y")
-    udt = rdt if U is None else _dt(U, "U")
-    _check(lib.wush_block_norm(ydt, rdt, udt, n, d, _ptr(Y), _ptr(w_post), kind, _ptr(gate), branch_scale, _ptr(R),
-                               res_scale, _ptr(w_pre), eps, _ptr(Rout), _ptr(U), _ptr(rstd_post), _ptr(rstd_pre),
-                               _stream(stream)), "wush_block_norm")
+    if w_pre is not None:
+        _want(w_pre, "w_pre", (d,), torch.float32)
+        wn = w_pre.data_ptr()
+    if Rout is not None:
+        _want(Rout, "Rout", shape, R.dtype)
+        ro = Rout.data_ptr()
+    if U is not None:
+        _want(U, "U", shape)
+        udt, u = _dt(U, "U"), U.data_ptr()
+    if rstd_post is not None:
+        _want(rstd_post, "rstd_post", (n,), torch.float32)
+        kp = rstd_post.data_ptr()
+    if rstd_pre is not None:
+        _want(rstd_pre, "rstd_pre", (n,), torch.float32)
+        kn = rstd_pre.data_ptr()
+    _check(lib.wush_block_norm(ydt, rdt, udt, n, d, y, wp, kind, g, branch_scale, R.data_ptr(), res_scale, wn, eps, ro,
+                               u, kp, kn, _stream(stream)), "wush_block_norm")
 
 
 def wush_block_norm_bwd_ws_bytes(n, d):
@@ -578,10 +595,10 @@ def wush_act8_swiglu_bwd(dH, g_codes, g_scales, u_codes, u_scales, dG, dU, strea
 
 def _adapters(seg_off, seg_adapter, A, Bt, rank, alpha):
     """(nseg, nad, rmax, d_in, d_out) of a set of adapters and the requests that use it."""
-    nad, rmax, d_in = A.shape
+    shape = nad, rmax, d_in = A.shape
     d_out = Bt.shape[-1]
     nseg = seg_adapter.shape[0]
-    _want(A, "A", (nad, rmax, d_in), torch.bfloat16)
+    _want(A, "A", shape, torch.bfloat16)
     _want(Bt, "Bt", (nad, rmax, d_out), torch.bfloat16)
     _want(seg_off, "seg_off", (nseg + 1,), torch.int32)
     _want(seg_adapter, "seg_adapter", (nseg,), torch.int32)
@@ -609,9 +626,10 @@ def wush_adapter_forward(X, seg_off, seg_adapter, A, Bt, rank, alpha, Y0, Y, V=N
     if V is not None:
         _want(V, "V", (n, rmax), torch.float32)
     wp, wb = _ws(ws)
-    _check(lib.wush_adapter_forward(_dt(X, "X"), _dt(Y, "Y"), n, d_in, d_out, _ptr(X), ldx, nseg, _ptr(seg_off),
-                                    _ptr(seg_adapter), nad, rmax, _ptr(A), _ptr(Bt), _ptr(rank), _ptr(alpha), _ptr(Y0),
-                                    ldy0, _ptr(Y), ldy, _ptr(V), wp, wb, _stream(stream)), "wush_adapter_forward")
+    _check(lib.wush_adapter_forward(_dt(X, "X"), _dt(Y, "Y"), n, d_in, d_out, X.data_ptr(), ldx, nseg,
+                                    seg_off.data_ptr(), seg_adapter.data_ptr(), nad, rmax, A.data_ptr(), Bt.data_ptr(),
+                                    rank.data_ptr(), alpha.data_ptr(), _ptr(Y0), ldy0, Y.data_ptr(), ldy, _ptr(V), wp,
+                                    wb, _stream(stream)), "wush_adapter_forward")
 
 
 def wush_adapter_backward_ws_bytes(n, d_in, d_out, nseg, nad, rmax):

@@ -69,7 +69,22 @@ struct NormArgs {
   float* k2;
 };
 
-template <class Y, class R, class U, int VPT>
+// Stores of eight values, past the caches where PAST.
+template <bool PAST>
+__device__ __forceinline__ void put8(float* p, const float* v) {
+  store8(p, v);   // two halves of lines: left to the caches to join
+}
+template <bool PAST>
+__device__ __forceinline__ void put8(bf16_t* p, const float* v) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(
+        u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])},
+        reinterpret_cast<u32x4*>(p));
+  else
+    store8(p, v);
+}
+
+template <class Y, class R, class U, int VPT, bool PAST>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kind, const Y* __restrict__ y,
                                                         const R* r, R* rout, U* __restrict__ u) {
   __shared__ float slots[2][16];
@@ -138,7 +153,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[v][i], x[v][i], s);
-    if (rout) store8(rout + base + col[v], x[v]);
+    if (rout) put8<PAST>(rout + base + col[v], x[v]);
   }
   if (!a.w_pre) return;
   block_sums<1>(&s, slots[1]);
@@ -151,7 +166,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
     load_weights(a.w_pre, col[v], w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] *= x[v][i] * k2;
-    store8(u + base + col[v], w);
+    put8<PAST>(u + base + col[v], w);
   }
 }
 
@@ -482,9 +497,11 @@ __global__ __launch_bounds__(1024) void norm_cols_kernel(int d, int parts, const
 
 constexpr int kMaxD = 24576;
 
-// Pieces of eight values per thread of the forward kernel: two, whose loads are
-// in flight together, up to the largest workgroup's 16384 columns.
-int fwd_vpt(int d) { return d <= 16384 ? 2 : 4; }
+// Pieces of eight values per thread of the forward kernel.  Few rows: one, up to
+// 8192 columns, since only the number of waves hides latency there (one row of
+// 4096: 3.2 against 4.1 us).  Many: two, whose loads are in flight together
+// (16384 rows of 5120: 156 against 171 us), four past 16384 columns.
+int fwd_vpt(int n, int d) { return n < 512 && d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
 
 // The backward kernel's: one up to 8192 columns.  Wider rows take more per
 // thread, and so many registers that only twelve waves (of 168) fit beyond 16384.
@@ -560,8 +577,14 @@ extern "C" wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtyp
     using YT = decltype(y);
     using RT = decltype(r);
     using UT = decltype(u);
-    auto k = fwd_vpt(d) == 2 ? norm_fwd_kernel<YT, RT, UT, 2> : norm_fwd_kernel<YT, RT, UT, 4>;
-    hipLaunchKernelGGL(k, dim3(n), dim3(threads(d, fwd_vpt(d))), 0, s, a, static_cast<int>(gate_kind), static_cast<const YT*>(Y),
+    const int vpt = fwd_vpt(n, d);
+    // outputs beyond the 256 MB of the last-level cache are written past it
+    const int64_t out = static_cast<int64_t>(n) * d * ((Rout ? sizeof(RT) : 0) + (U ? sizeof(UT) : 0));
+    const bool far = out > (int64_t{256} << 20);
+    auto k = vpt == 1   ? norm_fwd_kernel<YT, RT, UT, 1, false>
+             : vpt == 2 ? (far ? norm_fwd_kernel<YT, RT, UT, 2, true> : norm_fwd_kernel<YT, RT, UT, 2, false>)
+                        : (far ? norm_fwd_kernel<YT, RT, UT, 4, true> : norm_fwd_kernel<YT, RT, UT, 4, false>);
+    hipLaunchKernelGGL(k, dim3(n), dim3(threads(d, vpt)), 0, s, a, static_cast<int>(gate_kind), static_cast<const YT*>(Y),
                        static_cast<const RT*>(R), static_cast<RT*>(Rout), static_cast<UT*>(U));
     return launched(who);
   });
