@@ -123,8 +123,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without the Stream object around it (0.4 instead of 3 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _fmt(fmt):

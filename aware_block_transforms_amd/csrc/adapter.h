@@ -99,6 +99,133 @@ __device__ __forceinline__ Tile find_tile(int number, int n, int nseg, const int
   return t;
 }
 
+// What the grad kernel walks over, made once per backward call.
+// tokens [whole steps]: the tokens of adapter 0, 1, ..., each list in request
+//   order and padded to a multiple of 32 by its last token
+// count [nad]: an adapter's tokens (0 where its rank is)
+// start [nad + 1]: where its list begins, a multiple of 32
+// chunk [nad + 1]: the number of its first chunk
+// span [nad]: tokens of its chunks, whole steps
+// place [nseg]: where a request's tokens begin
+struct Lists {
+  int* tokens;
+  int* count;
+  int* start;
+  int* chunk;
+  int* span;
+  int* place;
+};
+
+__device__ __forceinline__ int lane_prefix(int v) {   // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int o = __shfl_up(v, m, 64);
+    if (lane >= m) v += o;
+  }
+  return v;
+}
+
+// Steps of a chunk at least, and the relative cost of a step: what the rows
+// take, and the products of each row tile.
+constexpr int kMinSteps = 4;
+__device__ __forceinline__ float step_cost(int rank, int rmax) {
+  const int tiles = (min(max(rank, 1), rmax) + 15) / 16;
+  return tiles > 4 ? 9.0f : tiles > 2 ? 6.0f : tiles > 1 ? 5.0f : 4.5f;
+}
+
+// Makes the lists; one workgroup of WAVES waves.  Its passes over the requests
+// depend on each other, and each takes a turn through memory: some 9 us in all,
+// which the low kernel of the backward call hides by giving it a workgroup of
+// its own.
+template <int WAVES>
+__device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, const int* ids, int nad, const int* rank,
+                                            int rmax, int chunks_wanted, const Lists& l) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto length = [&](int s, int a) {
+    if (s >= nseg || ids[s] != a) return 0;
+    return max(request_start(off, s + 1, nseg, n) - request_start(off, s, nseg, n), 0);
+  };
+  // one wave per adapter: its tokens (none where its rank is zero)
+  for (int a = wave; a < nad; a += WAVES) {
+    int sum = 0;
+    if (rank[a] > 0)
+      for (int b = 0; b < nseg; b += 64) sum = min(sum + length(b + lane, a), n);
+    sum = __shfl(lane_prefix(sum), 63, 64);
+    if (lane == 0) l.count[a] = min(sum, n);
+  }
+  __syncthreads();
+  if (wave == 0) {
+    // a list's cost: its tokens times the cost of a step at its rank
+    float cost = 0.0f;
+    int busy = 0;
+    for (int a = lane; a < nad; a += 64) {
+      cost += l.count[a] * step_cost(rank[a], rmax);
+      busy += l.count[a] > 0;
+    }
+    cost = wave_sum(cost);
+    busy = __shfl(lane_prefix(busy), 63, 64);
+    // every list ends inside a chunk, half of one wasted on average
+    const float share = cost / max(1, chunks_wanted - busy / 2);
+    int tokens = 0, chunks = 0, steps = 0;   // tokens: those that are not padding
+    for (int b = 0; b < nad; b += 64) {
+      const int a = b + lane;
+      // capped at n, which offsets that do not rise could pass
+      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(a < nad ? l.count[a] : 0));
+      const int to = static_cast<int>(min(past, static_cast<int64_t>(n)));
+      const int before = __shfl_up(to, 1, 64);
+      const int mine = to - (lane == 0 ? tokens : before);
+      const int span = a < nad ? 32 * max(kMinSteps, static_cast<int>(ceilf(share / (32.0f * step_cost(rank[a], rmax))))) : 32;
+      const int parts = (mine + span - 1) / span, c = lane_prefix(parts);
+      const int turns = (mine + 31) / 32, t = lane_prefix(turns);
+      if (a < nad) {
+        l.count[a] = mine;
+        l.span[a] = span;
+        l.start[a] = 32 * (steps + t - turns);
+        l.chunk[a] = chunks + c - parts;
+      }
+      tokens = __shfl(to, 63, 64);
+      steps += __shfl(t, 63, 64);
+      chunks += __shfl(c, 63, 64);
+    }
+    if (lane == 0) {
+      l.start[nad] = 32 * steps;
+      l.chunk[nad] = chunks;
+    }
+  }
+  __syncthreads();
+  for (int a = wave; a < nad; a += WAVES) {
+    const int room = l.count[a];
+    if (room == 0) continue;
+    int at = 0;
+    for (int b = 0; b < nseg; b += 64) {
+      const int m = length(b + lane, a), p = lane_prefix(m);
+      if (m > 0) l.place[b + lane] = min(at + p - m, room);
+      at = min(at + __shfl(p, 63, 64), room);
+    }
+  }
+  __syncthreads();
+  for (int s = wave; s < nseg; s += WAVES) {
+    const int a = ids[s];
+    if (a < 0 || a >= nad || l.count[a] == 0) continue;
+    const int first = request_start(off, s, nseg, n), m = request_start(off, s + 1, nseg, n) - first;
+    if (m <= 0) continue;
+    const int start = l.start[a], room = l.count[a], at = l.place[s];
+    for (int i = lane; i < m && at + i < room; i += 64) {
+      l.tokens[start + at + i] = first + i;
+      if (at + i == room - 1)
+        for (int q = room; q < (room + 31) / 32 * 32; ++q) l.tokens[start + q] = first + i;
+    }
+  }
+}
+
+// The lists wanted from a launch that has a workgroup to spare for them.
+struct ListJob {
+  bool on;
+  int chunks_wanted;
+  Lists l;
+};
+
 inline int64_t tile_numbers(int n, int T, int nseg) { return static_cast<int64_t>(n / T) + nseg; }
 
 }  // namespace wush

@@ -30,6 +30,7 @@ wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int
                           int64_t ldg, const void* X, const uint8_t* x_scales, int64_t ldx, int nseg,
                           const int* seg_off, const int* seg_adapter, int nad, int rmax, const int* rank,
                           const float* V, const float* dV, float* dA, float* dBt, void* ws, hipStream_t s);
+ListJob adapter_lists(int n, int d_in, int d_out, int nseg, int nad, int rmax, void* ws);
 bool adapter_grads_fit(int n, int d_in, int d_out, int nad, int rmax);
 size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax);
 }  // namespace wush
@@ -139,10 +140,14 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
                                                                   const bf16_t* __restrict__ factor,
                                                                   const int* __restrict__ rank,
                                                                   const float* __restrict__ alpha,
-                                                                  float* __restrict__ part) {
+                                                                  float* __restrict__ part, ListJob job) {
   constexpr int R = 16 * RT, T = 16 * TT;
   __shared__ float red[kWaves][16 * R];
-  const Tile t = find_tile<T>(blockIdx.x, n, nseg, off, ids, nad);
+  if (job.on && blockIdx.x == 0) {
+    if (blockIdx.y == 0) list_tokens<kWaves>(n, nseg, off, ids, nad, rank, R, job.chunks_wanted, job.l);
+    return;
+  }
+  const Tile t = find_tile<T>(blockIdx.x - job.on, n, nseg, off, ids, nad);
   if (t.begin >= t.end) return;
   float* out = part + (static_cast<int64_t>(blockIdx.y) * n + t.begin) * R;
   const int rows = t.end - t.begin;
@@ -484,22 +489,22 @@ int low_splits(int n, int d, int nseg, int rmax) {
 template <class X, int RT>
 void low_by_tiles(int tt, int splits, int n, int d, const void* x, int64_t ldx, int nseg, const int* off,
                   const int* ids, int nad, const void* factor, const int* rank, const float* alpha, float* part,
-                  hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(tile_numbers(n, 16 * tt, nseg)), splits);
+                  const ListJob& job, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(tile_numbers(n, 16 * tt, nseg) + job.on), splits);
   auto k = adapter_low_kernel<X, RT, 1>;
   if (tt == 2) k = adapter_low_kernel<X, RT, 2>;
   if (tt == 4) k = adapter_low_kernel<X, RT, RT == 8 ? 2 : 4>;
   hipLaunchKernelGGL(k, grid, dim3(64 * kWaves), 0, s, n, d, static_cast<const X*>(x), ldx, nseg, off, ids, nad,
-                     static_cast<const bf16_t*>(factor), rank, alpha, part);
+                     static_cast<const bf16_t*>(factor), rank, alpha, part, job);
 }
 
 template <class X>
 void low(int n, int d, const void* x, int64_t ldx, int nseg, const int* off, const int* ids, int nad, int rmax,
-         const void* factor, const int* rank, const float* alpha, float* part, hipStream_t s) {
+         const void* factor, const int* rank, const float* alpha, float* part, const ListJob& job, hipStream_t s) {
   auto f = rmax == 16 ? low_by_tiles<X, 1> : rmax == 32 ? low_by_tiles<X, 2> : rmax == 64 ? low_by_tiles<X, 4>
                                                                                          : low_by_tiles<X, 8>;
   f(low_tiles(n, nseg, rmax), low_splits(n, d, nseg, rmax), n, d, x, ldx, nseg, off, ids, nad, factor, rank, alpha,
-    part, s);
+    part, job, s);
 }
 
 template <class Y, int RT>
@@ -603,7 +608,7 @@ extern "C" wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int 
     if (e != hipSuccess) return fail(WUSH_E_HIP, "%s: scratch: %s", who, hipGetErrorString(e));
   }
   auto f = xdt == WUSH_F32 ? low<float> : low<bf16_t>;
-  f(n, d_in, X, ldx, nseg, seg_off, seg_adapter, nad, rmax, A, rank, alpha, part, s);
+  f(n, d_in, X, ldx, nseg, seg_off, seg_adapter, nad, rmax, A, rank, alpha, part, ListJob{}, s);
   wush_status out = launched(who);
   if (out == WUSH_OK) {
     auto g = ydt == WUSH_F32 ? spread<float> : spread<bf16_t>;
@@ -660,7 +665,8 @@ extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wus
   wush_status out = WUSH_OK;
   if (n > 0) {
     auto f = gdt == WUSH_F32 ? low<float> : low<bf16_t>;
-    f(n, d_out, dY, ldg, nseg, seg_off, seg_adapter, nad, rmax, Bt, rank, alpha, part, s);
+    f(n, d_out, dY, ldg, nseg, seg_off, seg_adapter, nad, rmax, Bt, rank, alpha, part,
+      adapter_lists(n, d_in, d_out, nseg, nad, rmax, rest), s);
     out = launched(who);
     if (out == WUSH_OK && dX) {
       auto g = ydt == WUSH_F32 ? spread<float> : spread<bf16_t>;

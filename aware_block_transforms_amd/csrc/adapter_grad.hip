@@ -2,10 +2,10 @@
 // adapter a of S[t][r] X[t][c], for (S, X, F) = (dV, X, A) and (V, dY, Bt).
 //
 // The sum runs over tokens, which lie along the slow axis of both operands, and
-// an adapter's tokens may be spread over many requests.  A first small kernel
-// lists the tokens of each adapter in order, each list padded to whole steps of
-// 32 tokens, and cuts it into chunks of several steps; a last one adds up the
-// chunks of an adapter in order, so that results do not depend on scheduling
+// an adapter's tokens may be spread over many requests.  So the tokens of each
+// adapter are listed in order first (list_tokens), each list padded to whole
+// steps of 32 tokens, and cut into chunks of several steps; a last kernel adds
+// up the chunks of an adapter in order, so that results do not depend on scheduling
 // (an adapter of one chunk is written directly).
 //
 // In a 16x16x32 product the eight k values of a lane are eight tokens.  A lane
@@ -32,119 +32,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kCols = 128 * kWaves;
 
-// tokens [whole steps]: the tokens of adapter 0, 1, ..., each list in request
-//   order and padded to a multiple of 32 by its last token
-// count [nad]: an adapter's tokens (0 where its rank is)
-// start [nad + 1]: where its list begins, a multiple of 32
-// chunk [nad + 1]: the number of its first chunk
-// span [nad]: tokens of its chunks, whole steps
-// place [nseg]: where a request's tokens begin
-struct Lists {
-  int* tokens;
-  int* count;
-  int* start;
-  int* chunk;
-  int* span;
-  int* place;
-};
-
-__device__ __forceinline__ int lane_prefix(int v) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int o = __shfl_up(v, m, 64);
-    if (lane >= m) v += o;
-  }
-  return v;
-}
-
-// Steps of a chunk at least, and the relative cost of a step: what the rows
-// take, and the products of each row tile.
-constexpr int kMinSteps = 4;
-__device__ __forceinline__ float step_cost(int rank, int rmax) {
-  const int tiles = (min(max(rank, 1), rmax) + 15) / 16;
-  return tiles > 4 ? 9.0f : tiles > 2 ? 6.0f : tiles > 1 ? 5.0f : 4.5f;
-}
-
-__global__ __launch_bounds__(1024) void adapter_list_kernel(int n, int nseg, const int* __restrict__ off,
-                                                            const int* __restrict__ ids, int nad,
-                                                            const int* __restrict__ rank, int rmax, int chunks_wanted, Lists l) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto length = [&](int s, int a) {
-    if (s >= nseg || ids[s] != a) return 0;
-    return max(request_start(off, s + 1, nseg, n) - request_start(off, s, nseg, n), 0);
-  };
-  // one wave per adapter: its tokens (none where its rank is zero)
-  for (int a = wave; a < nad; a += 16) {
-    int sum = 0;
-    if (rank[a] > 0)
-      for (int b = 0; b < nseg; b += 64) sum = min(sum + length(b + lane, a), n);
-    sum = __shfl(lane_prefix(sum), 63, 64);
-    if (lane == 0) l.count[a] = min(sum, n);
-  }
-  __syncthreads();
-  if (wave == 0) {
-    // a list's cost: its tokens times the cost of a step at its rank
-    float cost = 0.0f;
-    int busy = 0;
-    for (int a = lane; a < nad; a += 64) {
-      cost += l.count[a] * step_cost(rank[a], rmax);
-      busy += l.count[a] > 0;
-    }
-    cost = wave_sum(cost);
-    busy = __shfl(lane_prefix(busy), 63, 64);
-    // every list ends inside a chunk, half of one wasted on average
-    const float share = cost / max(1, chunks_wanted - busy / 2);
-    int tokens = 0, chunks = 0, steps = 0;   // tokens: those that are not padding
-    for (int b = 0; b < nad; b += 64) {
-      const int a = b + lane;
-      // capped at n, which offsets that do not rise could pass
-      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(a < nad ? l.count[a] : 0));
-      const int to = static_cast<int>(min(past, static_cast<int64_t>(n)));
-      const int before = __shfl_up(to, 1, 64);
-      const int mine = to - (lane == 0 ? tokens : before);
-      const int span = a < nad ? 32 * max(kMinSteps, static_cast<int>(ceilf(share / (32.0f * step_cost(rank[a], rmax))))) : 32;
-      const int parts = (mine + span - 1) / span, c = lane_prefix(parts);
-      const int turns = (mine + 31) / 32, t = lane_prefix(turns);
-      if (a < nad) {
-        l.count[a] = mine;
-        l.span[a] = span;
-        l.start[a] = 32 * (steps + t - turns);
-        l.chunk[a] = chunks + c - parts;
-      }
-      tokens = __shfl(to, 63, 64);
-      steps += __shfl(t, 63, 64);
-      chunks += __shfl(c, 63, 64);
-    }
-    if (lane == 0) {
-      l.start[nad] = 32 * steps;
-      l.chunk[nad] = chunks;
-    }
-  }
-  __syncthreads();
-  for (int a = wave; a < nad; a += 16) {
-    const int room = l.count[a];
-    if (room == 0) continue;
-    int at = 0;
-    for (int b = 0; b < nseg; b += 64) {
-      const int m = length(b + lane, a), p = lane_prefix(m);
-      if (m > 0) l.place[b + lane] = min(at + p - m, room);
-      at = min(at + __shfl(p, 63, 64), room);
-    }
-  }
-  __syncthreads();
-  for (int s = wave; s < nseg; s += 16) {
-    const int a = ids[s];
-    if (a < 0 || a >= nad || l.count[a] == 0) continue;
-    const int first = request_start(off, s, nseg, n), m = request_start(off, s + 1, nseg, n) - first;
-    if (m <= 0) continue;
-    const int start = l.start[a], room = l.count[a], at = l.place[s];
-    for (int i = lane; i < m && at + i < room; i += 64) {
-      l.tokens[start + at + i] = first + i;
-      if (at + i == room - 1)
-        for (int q = room; q < (room + 31) / 32 * 32; ++q) l.tokens[start + q] = first + i;
-    }
-  }
+// The lists of no tokens.
+__global__ __launch_bounds__(256) void adapter_list_kernel(int nseg, const int* off, const int* ids, int nad,
+                                                           const int* rank, int rmax, Lists l) {
+  list_tokens<4>(0, nseg, off, ids, nad, rank, rmax, 1, l);
 }
 
 // Adapter of a step or chunk `number`: the last one whose first is not past it.
@@ -449,6 +340,11 @@ int64_t step_numbers(int n, int nad) { return static_cast<int64_t>(n / 32) + nad
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
+size_t list_bytes(int n, int nseg, int nad) {
+  return round256(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4) + 4 * round256((static_cast<size_t>(nad) + 1) * 4) +
+         round256(static_cast<size_t>(nseg) * 4);
+}
+
 template <class X, class G, int RT>
 void launch(dim3 grid, const Side& a, const Side& b, int wgs_a, int nad, const int* rank, const Lists& l,
             hipStream_t s) {
@@ -465,9 +361,25 @@ auto by_rank(int rmax) {
 namespace wush {
 
 size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax) {
-  return round256(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4) + 4 * round256((static_cast<size_t>(nad) + 1) * 4) +
-         round256(static_cast<size_t>(nseg) * 4) +
+  return list_bytes(n, nseg, nad) +
          static_cast<size_t>(chunk_numbers(n, d_in, d_out, nad, rmax)) * rmax * (static_cast<size_t>(d_in) + d_out) * sizeof(float);
+}
+
+ListJob adapter_lists(int n, int d_in, int d_out, int nseg, int nad, int rmax, void* ws) {
+  char* p = static_cast<char*>(ws);
+  auto take = [&](size_t count) {
+    int* at = reinterpret_cast<int*>(p);
+    p += round256(count * 4);
+    return at;
+  };
+  ListJob job{true, chunks_wanted(n, d_in, d_out, rmax), {}};
+  job.l.tokens = take(static_cast<size_t>(step_numbers(n, nad)) * 32);
+  job.l.count = take(static_cast<size_t>(nad) + 1);
+  job.l.start = take(static_cast<size_t>(nad) + 1);
+  job.l.chunk = take(static_cast<size_t>(nad) + 1);
+  job.l.span = take(static_cast<size_t>(nad) + 1);
+  job.l.place = take(nseg);
+  return job;
 }
 
 bool adapter_grads_fit(int n, int d_in, int d_out, int nad, int rmax) {
@@ -479,24 +391,14 @@ wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int
                           const int* seg_off, const int* seg_adapter, int nad, int rmax, const int* rank,
                           const float* V, const float* dV, float* dA, float* dBt, void* ws, hipStream_t s) {
   const int64_t numbers = chunk_numbers(n, d_in, d_out, nad, rmax);
-  char* p = static_cast<char*>(ws);
-  auto take = [&](size_t bytes) {
-    char* at = p;
-    p += round256(bytes);
-    return at;
-  };
-  Lists l;
-  l.tokens = reinterpret_cast<int*>(take(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4));
-  l.count = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
-  l.start = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
-  l.chunk = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
-  l.span = reinterpret_cast<int*>(take((static_cast<size_t>(nad) + 1) * 4));
-  l.place = reinterpret_cast<int*>(take(static_cast<size_t>(nseg) * 4));
-  float* part = reinterpret_cast<float*>(p);
+  const ListJob job = adapter_lists(n, d_in, d_out, nseg, nad, rmax, ws);
+  const Lists& l = job.l;
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + list_bytes(n, nseg, nad));
   const Side a{X, x_scales, dV, dA, part, ldx, d_in};
   const Side b{dY, nullptr, V, dBt, part + numbers * rmax * d_in, ldg, d_out};
-  hipLaunchKernelGGL(adapter_list_kernel, dim3(1), dim3(1024), 0, s, n, nseg, seg_off, seg_adapter, nad, rank, rmax,
-                     chunks_wanted(n, d_in, d_out, rmax), l);
+  // with tokens, the low kernel has made the lists
+  if (n == 0)
+    hipLaunchKernelGGL(adapter_list_kernel, dim3(1), dim3(256), 0, s, nseg, seg_off, seg_adapter, nad, rank, rmax, l);
   const int wgs_a = (d_in + kCols - 1) / kCols, wgs_b = (d_out + kCols - 1) / kCols;
   if (n > 0) {
     const dim3 grid(wgs_a + wgs_b, static_cast<unsigned>(numbers));
