@@ -422,8 +422,10 @@ __device__ __forceinline__ void spread_columns(const SpreadTile& t, int n, int d
   } while (TT == 1 && c0 < d);
 }
 
+// Short requests live on the number of waves: three a SIMD, where the factor's
+// operands leave the registers for it (64 requests on 12288 columns: 14.6 against 16.5 us).
 template <class Y, int RT, int TT, bool BASE, bool PAST>
-__global__ __launch_bounds__(64 * kWaves) void adapter_spread_kernel(int n, int d, int col_wgs,
+__global__ __launch_bounds__(64 * kWaves, TT == 1 && RT * YRow<Y>::CW <= 16 ? 3 : 1) void adapter_spread_kernel(int n, int d, int col_wgs,
                                                                      const float* __restrict__ part, int splits,
                                                                      int nseg, const int* __restrict__ off,
                                                                      const int* __restrict__ ids, int nad,
@@ -475,13 +477,16 @@ int low_tiles(int n, int nseg, int rmax) {
 // built once for four tiles; 16 where requests are short.
 bool short_requests(int n, int nseg) { return n / nseg <= 16; }
 
-// Workgroups along k: four for every compute unit over the whole grid, while
-// each of their waves still has a piece of 64 values of its own.
+// Workgroups along k: three for every compute unit over the whole grid, in one
+// round, while each of their waves still has a piece of 64 values of its own.
+// Whoever reads V adds their parts up, at most nine for short requests (4096 in:
+// one token 7.9 against 8.7 us with 16, both kernels) and 16 for long ones.
 int low_splits(int n, int d, int nseg, int rmax) {
-  const int64_t tiles = tile_numbers(n, 16 * low_tiles(n, nseg, rmax), nseg);
-  const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves);
+  const int tt = low_tiles(n, nseg, rmax);
+  const int64_t tiles = tile_numbers(n, 16 * tt, nseg);
+  const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves), most = tt == 1 ? 9 : 16;
   int s = static_cast<int>(768 / tiles);
-  if (s > 16) s = 16;
+  if (s > most) s = most;
   if (s > pieces) s = pieces;
   return s < 1 ? 1 : s;
 }
@@ -513,9 +518,9 @@ void spread_by_tiles(bool one, int n, int d, const float* part, int splits, int 
                      float* V, hipStream_t s) {
   const int cols = 16 * YRow<Y>::CW * kWaves, tokens = one ? 16 : 64;
   // short requests: a workgroup takes several column blocks in turn, so that
-  // at most four for every compute unit (one round of them) do it all
+  // the three that fit every compute unit do it all in one round
   const int64_t tiles = tile_numbers(n, tokens, nseg);
-  const int all = (d + cols - 1) / cols, few = tiles < 1024 ? static_cast<int>(1024 / tiles) : 1;
+  const int all = (d + cols - 1) / cols, few = tiles < 768 ? static_cast<int>(768 / tiles) : 1;
   const int col_wgs = one && few < all ? few : all;
   const dim3 grid(static_cast<unsigned>(col_wgs * tiles));
   // Y beyond the 256 MB of the last-level cache goes past the caches, which keep

@@ -1,6 +1,6 @@
-"""Allocation helpers around the libwush calls for one quantized linear layer.
+"""Allocation helpers around the libwush calls for one quantized linear layer and the adapters beside it.
 
-``W4A4Layer`` holds the device-resident pieces of one layer (transform
+``AdapterSet`` holds low-rank adapters of one projection.  ``W4A4Layer`` holds the device-resident pieces of one layer (transform
 matrices, packed weight codes and scales) and exposes the online path
 (transform + quantize activations, then the W4A4 matmul) as two library
 calls.  Tensors come from torch's caching allocator; every byte of
@@ -76,10 +76,76 @@ class W4A4Layer:
         W.wush_w4a4_gemm(self.fmt, codes, scales, self.w_codes, self.w_scales, Y, a_g=self.x_g, b_g=self.w_g,
                          ws=self._ws if need else None)
 
-    def forward(self, X, out=None):
+    def forward(self, X, out=None, adapters=None, requests=None):
+        """X W^T from the quantized operands; with an AdapterSet and the requests that X is made of, their adapters
+        are added to it in place."""
         n = X.shape[0]
         codes, scales = self.alloc_activation_codes(n, X.device)
         self.quantize(X, codes, scales)
         Y = out if out is not None else torch.empty((n, self.d_out), dtype=torch.float32, device=X.device)
         self.matmul(codes, scales, Y)
+        if adapters is not None:
+            adapters.forward(X, requests, Y, out=Y)
         return Y
+
+
+def request_table(lengths, adapters, device="cuda"):
+    """(offsets, adapter ids) on the device: request i has lengths[i] tokens and adapter adapters[i], -1 for none."""
+    off = np.concatenate(([0], np.cumsum(np.asarray(lengths, np.int64)))).astype(np.int32)
+    return torch.from_numpy(off).to(device), torch.tensor(adapters, dtype=torch.int32, device=device)
+
+
+class AdapterSet:
+    """Low-rank adapters beside one projection d_in -> d_out, and their workspaces.
+
+    ``A`` [nad][rmax][d_in] and ``Bt`` [nad][rmax][d_out] are bfloat16 (Bt is the transpose of the usual B and starts at
+    zero), ``rank`` and ``alpha`` per adapter.  A request table (see ``request_table``) says whose tokens are whose.
+    """
+
+    def __init__(self, nad, rmax, d_in, d_out, rank=None, alpha=1.0, device="cuda", seed=0):
+        self.nad, self.rmax, self.d_in, self.d_out = nad, rmax, d_in, d_out
+        r = np.random.default_rng([seed, nad, d_in])
+        A = (r.standard_normal((nad, rmax, d_in)) / np.sqrt(d_in)).astype(np.float32)
+        self.A = torch.from_numpy(A).to(device).to(torch.bfloat16)
+        self.Bt = torch.zeros((nad, rmax, d_out), dtype=torch.bfloat16, device=device)
+        self.rank = torch.tensor([rmax] * nad if rank is None else list(rank), dtype=torch.int32, device=device)
+        self.alpha = torch.tensor([float(alpha)] * nad if np.isscalar(alpha) else list(alpha), dtype=torch.float32,
+                                  device=device)
+        self._ws = None   # grown on demand
+
+    def _scratch(self, need, device):
+        if self._ws is None or self._ws.numel() < need or self._ws.device != device:
+            self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return self._ws
+
+    def forward(self, X, requests, Y0, out=None, keep=False):
+        """Y = Y0 + alpha X A^T Bt, per request; with ``keep`` also V, which the backward pass needs."""
+        off, ids = requests
+        n = X.shape[0]
+        Y = out if out is not None else torch.empty_like(Y0)
+        V = torch.empty((n, self.rmax), dtype=torch.float32, device=X.device) if keep else None
+        ws = self._scratch(W.wush_adapter_ws_bytes(n, self.d_in, ids.shape[0], self.rmax), X.device)
+        W.wush_adapter_forward(X, off, ids, self.A, self.Bt, self.rank, self.alpha, Y0, Y, V=V, ws=ws)
+        return (Y, V) if keep else Y
+
+    def backward(self, dY, X, requests, V, dX0=None, x_scales=None, dx_dtype=torch.bfloat16):
+        """(dX, dA, dBt); X may be the codes of an act8 checkpoint, with their scales in ``x_scales``."""
+        off, ids = requests
+        n, dev = dY.shape[0], dY.device
+        dX = torch.empty((n, self.d_in), dtype=dx_dtype if dX0 is None else dX0.dtype, device=dev)
+        dA = torch.empty((self.nad, self.rmax, self.d_in), dtype=torch.float32, device=dev)
+        dBt = torch.empty((self.nad, self.rmax, self.d_out), dtype=torch.float32, device=dev)
+        ws = self._scratch(W.wush_adapter_backward_ws_bytes(n, self.d_in, self.d_out, ids.shape[0], self.nad, self.rmax),
+                           dev)
+        W.wush_adapter_backward(dY, X, off, ids, self.A, self.Bt, self.rank, self.alpha, V, dX0, dX, dA, dBt,
+                                x_scales=x_scales, ws=ws)
+        return dX, dA, dBt
+
+
+def act8_store(X):
+    """(codes, scales) of an act8 checkpoint of X."""
+    n, d = X.shape
+    codes = torch.empty((n, d), dtype=torch.int8, device=X.device)
+    scales = torch.empty((n, d // 32), dtype=torch.uint8, device=X.device)
+    W.wush_act8_pack(X, codes, scales)
+    return codes, scales
