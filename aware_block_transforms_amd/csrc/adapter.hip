@@ -41,95 +41,124 @@ constexpr int kWaves = 4;
 
 // ---------------------------------------------------------------------------
 // low: V[t][r] = alpha sum_k X[t][k] A[r][k], by 16x16x32 products of token
-// rows with factor rows, both read with k along the row.  A workgroup takes
-// 16 TT tokens; its four waves and the grid's y share k in pieces of 64, each
-// lane 16 neighbouring values of a row (two products; which k a lane holds
-// does not matter as long as both operands agree).  The waves' sums are joined
-// through LDS, those of the y workgroups lie in `part` [gridDim.y][n][R] and
-// are added by whoever reads V.  Rows past the tile's tokens or the rank
-// repeat the last one, so no load needs a guard; their results are dropped.
+// rows with factor rows, both with k along the row.  A workgroup takes 16 TT
+// tokens; its four waves and the grid's y share k in pieces of 64.  The waves'
+// sums are joined through LDS, those of the y workgroups lie in `part`
+// [gridDim.y][n][R] and are added by whoever reads V.
+//
+// An operand wants 16 rows side by side in neighbouring lanes, and loaded that
+// way every lane is an access of its own to the first-level cache, which then
+// bounds the kernel.  So a wave loads its pieces in whole 128-byte lines (eight
+// lanes a row) and takes the operands out of its own part of LDS, where the
+// 16-byte chunks of row r are kept in the order c ^ (r mod the row's chunks), so
+// that the eight or sixteen rows of a read fall into different banks.  The next
+// piece is on its way, in registers, during the products of the one in LDS; no
+// barrier is needed.  Rows past the tile's tokens or the rank, and columns past
+// d, lie outside the buffer resources and come as zeros.
 
-template <class T>
-struct XOps;
-template <>
-struct XOps<bf16_t> {
-  static constexpr int kTerms = 1;
-  u32x4 v[2];
-  __device__ __forceinline__ void load(const bf16_t* p) {
-    v[0] = reinterpret_cast<const u32x4*>(p)[0];
-    v[1] = reinterpret_cast<const u32x4*>(p)[1];
+// A piece of 64 columns of 16 N rows: C 16-byte chunks a row.
+template <class T, int N>
+struct Piece {
+  static constexpr int C = is_f32<T> ? 16 : 8, kRows = 64 / C, kLoads = 16 * N / kRows, kBytes = 16 * N * C * 16;
+  static constexpr int kValues = 16 / sizeof(T);   // of a chunk
+  __amdgpu_buffer_rsrc_t from;
+  uint32_t lane_at, stride, columns;
+  u32x4 v[kLoads];
+
+  // `rows` rows of d values, ld apart
+  __device__ __forceinline__ void open(const T* p, int rows, int d, int64_t ld) {
+    const int lane = threadIdx.x & 63;
+    from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), static_cast<short>(0),
+                                             ((rows - 1) * static_cast<int>(ld) + d) * static_cast<int>(sizeof(T)), 0x00020000);
+    stride = static_cast<uint32_t>(kRows * ld * sizeof(T));
+    lane_at = static_cast<uint32_t>((lane / C) * ld * sizeof(T)) + lane % C * 16;
+    columns = d;
   }
-  __device__ __forceinline__ void load_tail(const bf16_t* p, int left) {
+  // the used row tiles' loads, at column k; the rows count in the vector offset,
+  // which is what the range check is sure to see
+  template <int USED>
+  __device__ __forceinline__ void load(int k) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) v[h] = left > 8 * h ? reinterpret_cast<const u32x4*>(p)[h] : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < USED * 16 / kRows; ++i)
+      v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, lane_at + i * stride, k * sizeof(T), 0));
   }
-  __device__ __forceinline__ void operand(int h, u32x4 (&t)[3]) const { t[0] = v[h]; }
-};
-template <>
-struct XOps<float> {
-  static constexpr int kTerms = 3;
-  f32x4 v[4];
-  __device__ __forceinline__ void load(const float* p) {
+  // the same for a piece that runs past the last column
+  template <int USED>
+  __device__ __forceinline__ void load_tail(int k) {
+    const uint32_t at = k + (threadIdx.x & 63) % C * kValues < columns ? lane_at : 0x80000000u;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) v[h] = reinterpret_cast<const f32x4*>(p)[h];
+    for (int i = 0; i < USED * 16 / kRows; ++i)
+      v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at + i * stride, k * sizeof(T), 0));
   }
-  __device__ __forceinline__ void load_tail(const float* p, int left) {
+  template <int USED>
+  __device__ __forceinline__ void put(u32x4* lds) const {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int h = 0; h < 4; ++h)
-      v[h] = left > 4 * h ? reinterpret_cast<const f32x4*>(p)[h] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  __device__ __forceinline__ void operand(int h, u32x4 (&t)[3]) const {
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = v[2 * h][i];
-      x[4 + i] = v[2 * h + 1][i];
+    for (int i = 0; i < USED * 16 / kRows; ++i) {
+      const int r = i * kRows + lane / C;
+      lds[r * C + (lane % C ^ r % C)] = v[i];
     }
-    split8(x, t);
   }
 };
 
-// The product over a wave's pieces of k, for NT row tiles of the factor.
+// The operand of row tile i and k half h, lane 16 g + j: columns 8 (4 h + g) ..
+// of row 16 i + j.
+__device__ __forceinline__ void low_operand(const u32x4* lds, int i, int h, u32x4 (&t)[1], bf16_t) {
+  const int lane = threadIdx.x & 63, r = 16 * i + (lane & 15), c = 4 * h + (lane >> 4);
+  t[0] = lds[r * 8 + (c ^ r % 8)];
+}
+__device__ __forceinline__ void low_operand(const u32x4* lds, int i, int h, u32x4 (&t)[3], float) {
+  const int lane = threadIdx.x & 63, r = 16 * i + (lane & 15), c = 2 * (4 * h + (lane >> 4));
+  const f32x4 a = __builtin_bit_cast(f32x4, lds[r * 16 + (c ^ r % 16)]);
+  const f32x4 b = __builtin_bit_cast(f32x4, lds[r * 16 + ((c + 1) ^ r % 16)]);
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  split8(v, t);
+}
+
+// The products of a wave's pieces of k, for NT row tiles of the factor.
 template <class X, int NT, int RT, int TT>
-__device__ __forceinline__ void low_pieces(const X* const (&xp)[TT], const bf16_t* const (&fp)[RT], int k, int d,
-                                           int step, f32x4 (&acc)[TT][RT]) {
-  struct Piece {
-    XOps<X> x[TT];
-    XOps<bf16_t> f[NT];
-  };
-  const int g = (threadIdx.x & 63) >> 4;
-  auto load = [&](Piece& p, int at) {
+__device__ __forceinline__ void low_pieces(Piece<X, TT>& x, Piece<bf16_t, RT>& f, int k, int d, int step, u32x4* lds,
+                                           f32x4 (&acc)[TT][RT]) {
+  constexpr int kTerms = is_f32<X> ? 3 : 1;
+  u32x4 *xl = lds, *fl = lds + Piece<X, TT>::kBytes / 16;
+  auto multiply = [&]() {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) p.x[i].load(xp[i] + at);
+    for (int h = 0; h < 2; ++h) {
+      u32x4 ft[NT][1];
 #pragma unroll
-    for (int r = 0; r < NT; ++r) p.f[r].load(fp[r] + at);
-  };
-  auto multiply = [&](const Piece& p) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int r = 0; r < NT; ++r) low_operand(fl, r, h, ft[r], bf16_t());
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
-        u32x4 xt[3];
-        p.x[i].operand(h, xt);
+        u32x4 xt[kTerms];
+        low_operand(xl, i, h, xt, X());
 #pragma unroll
-        for (int m = 0; m < XOps<X>::kTerms; ++m)
+        for (int m = 0; m < kTerms; ++m)
 #pragma unroll
-          for (int r = 0; r < NT; ++r) acc[i][r] = mfma(xt[m], p.f[r].v[h], acc[i][r]);
+          for (int r = 0; r < NT; ++r) acc[i][r] = mfma(xt[m], ft[r][0], acc[i][r]);
       }
+    }
   };
-  for (; k + 64 <= d; k += step) {
-    Piece p;
-    load(p, k);
-    multiply(p);
+  const int whole = k + 64 <= d ? (d - 64 - k) / step + 1 : 0;
+  if (whole > 0) {
+    x.template load<TT>(k);
+    f.template load<NT>(k);
+    for (int i = 0; i < whole; ++i) {
+      x.template put<TT>(xl);
+      f.template put<NT>(fl);
+      // past the last piece it is loaded again: a branch would cost a wait
+      const int next = k + min(i + 1, whole - 1) * step;
+      x.template load<TT>(next);
+      f.template load<NT>(next);
+      multiply();
+    }
   }
+  k += whole * step;
   if (k < d) {
-    Piece p;
-    const int left = d - k - 16 * g;
-#pragma unroll
-    for (int i = 0; i < TT; ++i) p.x[i].load_tail(xp[i] + k, left);
-#pragma unroll
-    for (int r = 0; r < NT; ++r) p.f[r].load_tail(fp[r] + k, left);
-    multiply(p);
+    x.template load_tail<TT>(k);
+    f.template load_tail<NT>(k);
+    x.template put<TT>(xl);
+    f.template put<NT>(fl);
+    multiply();
   }
 }
 
@@ -142,7 +171,9 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
                                                                   const float* __restrict__ alpha,
                                                                   float* __restrict__ part, ListJob job) {
   constexpr int R = 16 * RT, T = 16 * TT;
-  __shared__ float red[kWaves][16 * R];
+  // a wave's pieces, and after the products its sums of one token tile
+  constexpr int kPieces = (Piece<X, TT>::kBytes + Piece<bf16_t, RT>::kBytes) / 16, kSums = 16 * R / 4;
+  __shared__ u32x4 lds[kWaves][kPieces > kSums ? kPieces : kSums];
   if (job.on && blockIdx.x == 0) {
     if (blockIdx.y == 0) list_tokens<kWaves>(n, nseg, off, ids, nad, rank, R, job.chunks_wanted, job.l);
     return;
@@ -158,31 +189,28 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
   }
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const X* xp[TT];
-  const bf16_t* fp[RT];
-#pragma unroll
-  for (int i = 0; i < TT; ++i) xp[i] = x + static_cast<int64_t>(min(t.begin + 16 * i + j, t.end - 1)) * ldx + 16 * g;
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    fp[i] = factor + (static_cast<int64_t>(t.adapter) * R + min(16 * i + j, rk - 1)) * d + 16 * g;
+  Piece<X, TT> xp;
+  Piece<bf16_t, RT> fp;
+  xp.open(x + t.begin * ldx, rows, d, ldx);
+  fp.open(factor + static_cast<int64_t>(t.adapter) * R * d, rk, d, d);
   f32x4 acc[TT][RT];
 #pragma unroll
   for (int i = 0; i < TT; ++i)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[i][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int step = 64 * kWaves * gridDim.y, k = 64 * (kWaves * blockIdx.y + wave);
-  // row tiles in use, rounded up to a power of two; the extra ones repeat the
-  // last row and are dropped
+  // row tiles in use, rounded up to a power of two
   const int tiles = (rk + 15) / 16;
   if (RT > 4 && tiles > 4)
-    low_pieces<X, RT, RT, TT>(xp, fp, k, d, step, acc);
+    low_pieces<X, RT, RT, TT>(xp, fp, k, d, step, lds[wave], acc);
   else if (RT > 2 && tiles > 2)
-    low_pieces<X, (RT > 4 ? 4 : RT), RT, TT>(xp, fp, k, d, step, acc);
+    low_pieces<X, (RT > 4 ? 4 : RT), RT, TT>(xp, fp, k, d, step, lds[wave], acc);
   else if (RT > 1 && tiles > 1)
-    low_pieces<X, (RT > 2 ? 2 : RT), RT, TT>(xp, fp, k, d, step, acc);
+    low_pieces<X, (RT > 2 ? 2 : RT), RT, TT>(xp, fp, k, d, step, lds[wave], acc);
   else
-    low_pieces<X, 1, RT, TT>(xp, fp, k, d, step, acc);
+    low_pieces<X, 1, RT, TT>(xp, fp, k, d, step, lds[wave], acc);
   const float f = alpha[t.adapter];
+  auto sums = [&](int w) { return reinterpret_cast<float*>(lds[w]); };
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     if (16 * i >= rows) break;
@@ -190,13 +218,13 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][(4 * g + e) * R + 16 * r + j] = acc[i][r][e];
+      for (int e = 0; e < 4; ++e) sums(wave)[(4 * g + e) * R + 16 * r + j] = acc[i][r][e];
     __syncthreads();
     const int count = min(rows - 16 * i, 16) * R;
     for (int q = threadIdx.x; q < count; q += 64 * kWaves) {
-      float s = red[0][q];
+      float s = sums(0)[q];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += red[w][q];
+      for (int w = 1; w < kWaves; ++w) s += sums(w)[q];
       out[16 * i * R + q] = q % R < rk ? f * s : 0.0f;
     }
   }
@@ -554,7 +582,7 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kMaxSeg = 1 << 20;
 constexpr int kMaxTokens = 1 << 24;   // so that sums over 64 requests stay in 32 bits
-// Row strides of Y and Y0: the 64 rows of a workgroup stay below 2^31 bytes.
+// Row strides: the 64 rows of a workgroup stay below 2^31 bytes.
 constexpr int64_t kMaxStride = 1 << 22;
 
 // X as the grad kernel sees it: the two float types and the act8 codes.
@@ -598,8 +626,8 @@ extern "C" wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int 
   if (st != WUSH_OK) return st;
   if (ldx < d_in || ldx % 8 || ldy < d_out || ldy % 8 || (Y0 && (ldy0 < d_out || ldy0 % 8)))
     return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
-  if (ldy > kMaxStride || (Y0 && ldy0 > kMaxStride))
-    return fail(WUSH_E_SHAPE, "%s: rows of Y above %lld values", who, static_cast<long long>(kMaxStride));
+  if (ldx > kMaxStride || ldy > kMaxStride || (Y0 && ldy0 > kMaxStride))
+    return fail(WUSH_E_SHAPE, "%s: row strides above %lld values", who, static_cast<long long>(kMaxStride));
   if (n == 0) return WUSH_OK;
   if (!X || !seg_off || !seg_adapter || !A || !Bt || !rank || !alpha || !Y) return fail(WUSH_E_ARG, "%s: null pointer", who);
   for (const void* p : {X, A, Bt, Y0, static_cast<const void*>(Y), static_cast<const void*>(V), static_cast<const void*>(ws)})
@@ -645,8 +673,8 @@ extern "C" wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wus
   if (ldg < d_out || ldg % 8 || ldx < d_in || ldx % 8 || (dX && (lddx < d_in || lddx % 8)) ||
       (dX && dX0 && (lddx0 < d_in || lddx0 % 8)))
     return fail(WUSH_E_SHAPE, "%s: row strides must be multiples of 8, at least the row's length", who);
-  if (dX && (lddx > kMaxStride || (dX0 && lddx0 > kMaxStride)))
-    return fail(WUSH_E_SHAPE, "%s: rows of dX above %lld values", who, static_cast<long long>(kMaxStride));
+  if (ldg > kMaxStride || (dX && (lddx > kMaxStride || (dX0 && lddx0 > kMaxStride))))
+    return fail(WUSH_E_SHAPE, "%s: row strides above %lld values", who, static_cast<long long>(kMaxStride));
   if (!adapter_grads_fit(n, d_in, d_out, nad, rmax)) return fail(WUSH_E_SHAPE, "%s: nad=%d passes the launch limit", who, nad);
   if (x_scales && (d_in % 32 || ldx != d_in))
     return fail(WUSH_E_SHAPE, "%s: an act8 checkpoint has whole groups of 32 and no row stride of its own", who);
