@@ -555,3 +555,62 @@ def test_offsets_beyond_32_bits():
     W.wush_block_norm(tail, w, None, tail, w, None, y2)
     torch.cuda.synchronize()
     assert torch.equal(U[n - k:], y2)
+
+
+def test_gradient_offsets_beyond_32_bits():
+    # 2.4e9 values of X, only the last tokens with a gradient: the sums are those of a short call on them
+    n, d, k = 140000, 17408, 40
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    tail = torch.randn((k, d), generator=g, device=DEV).to(torch.bfloat16)
+    X = torch.full((n, d), 0.5, dtype=torch.bfloat16, device=DEV)
+    X[n - k:] = tail
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    A = torch.randn((1, 16, d), generator=g, device=DEV).mul_(0.01).to(torch.bfloat16)
+    Bt = torch.randn((1, 16, 64), generator=g, device=DEV).mul_(0.1).to(torch.bfloat16)
+    rank, alpha = i32([16]), torch.ones(1, device=DEV)
+    dY, V = torch.zeros((n, 64), device=DEV), torch.zeros((n, 16), device=DEV)
+    dY[n - k:] = torch.randn((k, 64), generator=g, device=DEV)
+    V[n - k:] = torch.randn((k, 16), generator=g, device=DEV)
+    c, s = torch.empty((n, d), dtype=torch.int8, device=DEV), torch.empty((n, d // 32), dtype=torch.uint8, device=DEV)
+    W.wush_act8_pack(X, c, s)
+    for x, xs, xt in ((X, None, tail.double()), (c, s, bo.act8_values(c[n - k:].cpu().numpy(), s[n - k:].cpu().numpy()))):
+        dA, dB = new(1, 16, d), new(1, 16, 64)
+        W.wush_adapter_backward(dY, x, i32([0, n]), i32([0]), A, Bt, rank, alpha, V, None, None, dA, dB, x_scales=xs)
+        torch.cuda.synchronize()
+        xt = f64(xt) if torch.is_tensor(xt) else xt
+        ref, mag = bo.adapter_backward(f64(dY[n - k:]), xt, [0, k], [0], f64(A), f64(Bt), [16], [1.0], f64(V[n - k:]), None)
+        near(dA, ref[1], mag[1], 64 + k, "dA")
+        near(dB, ref[2], mag[2], k, "dBt")
+
+
+def test_nothing_to_do():
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device=DEV)  # noqa: E731
+    w = z(64)
+    W.wush_block_norm(z(0, 64), w, None, z(0, 64), w, z(0, 64), z(0, 64))
+    W.wush_act8_pack(z(0, 64), z(0, 64, dt=torch.int8), z(0, 2, dt=torch.uint8))
+    W.wush_act8_swiglu(z(0, 64), z(0, 64), z(0, 64))
+    A = z(1, 16, 64, dt=torch.bfloat16)
+    W.wush_adapter_forward(z(0, 64), z(2, dt=torch.int32), z(1, dt=torch.int32), A, A, z(1, dt=torch.int32), z(1), None,
+                           z(0, 64))
+    torch.cuda.synchronize()
+
+
+def test_tokens_without_an_adapter_are_not_read():
+    # NaN in the rows of requests without an adapter reaches nothing but their own base values
+    c = Case(70, 200, 264, 136, 5, 2, 32, ranks=[32, 17])
+    c.off, c.ids = [0, 60, 61, 130, 180, 200], [0, -1, 1, 7, 0]
+    c.dev = (torch.tensor(c.off, dtype=torch.int32, device=DEV), torch.tensor(c.ids, dtype=torch.int32, device=DEV)) + c.dev[2:]
+    clean, cv = c.forward()
+    dY = dev(c.r.standard_normal((200, 136)), "bf16")
+    out = []
+    for bad in (False, True):
+        if bad:
+            c.X[60], c.X[130:180], dY[60], dY[130:180] = float("nan"), float("inf"), float("inf"), float("nan")
+            Y, V = c.forward()
+            assert torch.equal(Y, clean) and torch.equal(V, cv)
+        dX, dA, dB = new(200, 264), new(2, 32, 264), new(2, 32, 136)
+        W.wush_adapter_backward(dY, c.X, *c.dev, cv, None, dX, dA, dB)
+        torch.cuda.synchronize()
+        out.append((dX, dA, dB))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
