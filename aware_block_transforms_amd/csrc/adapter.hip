@@ -278,11 +278,19 @@ struct SpreadTile {
 template <int RT, int TT>
 using SpreadOps = u32x4[TT][(RT + 1) / 2][RT == 1 ? 2 : 3][64];
 
-__device__ __forceinline__ void add8(float* v, const raw8<float>& r) {
+// Where lane 16 g + j's 16 bytes of an operand lie.  Neighbouring threads of
+// stage_v write neighbouring lane groups, which without the exchange would fall
+// into the same banks.
+template <int RT>
+__device__ __forceinline__ int spread_slot(int ks, int g, int j) {
+  return 16 * g + (j ^ (RT == 1 ? 4 * (g & 1) : 2 * g + (ks & 1)));
+}
+
+__device__ __forceinline__ void add8(float* v, const raw8<float>& r, bool counts) {
   float w[8];
   widen8(r, w);
 #pragma unroll
-  for (int x = 0; x < 8; ++x) v[x] += w[x];
+  for (int x = 0; x < 8; ++x) v[x] += counts ? w[x] : 0.0f;
 }
 
 // Adds up the parts of V for the tile's tokens and puts its operands into LDS.
@@ -297,20 +305,21 @@ __device__ __forceinline__ void stage_v(const SpreadTile& t, int n, const float*
     float v[8] = {};
     if (row < t.rows) {
       const int64_t at = (static_cast<int64_t>(t.begin) + row) * R + 8 * r8;
-      raw8<float> r;
-      load8(r, part + at);
-      widen8(r, v);
-      int i = 1;
-      for (; i + 3 < splits; i += 4) {   // four loads in flight
-        raw8<float> o[4];
+      // four loads in flight, then those left together: each turn through memory
+      // costs most of a microsecond
+      raw8<float> o[4];
+      int i = 0;
+      for (; i + 3 < splits; i += 4) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) load8(o[k], part + at + (i + k) * v_step);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add8(v, o[k]);
+        for (int k = 0; k < 4; ++k) add8(v, o[k], true);
       }
-      for (; i < splits; ++i) {
-        load8(r, part + at + i * v_step);
-        add8(v, r);
+      if (i < splits) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) load8(o[k], part + at + min(i + k, splits - 1) * v_step);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) add8(v, o[k], i + k < splits);
       }
       // V itself, where the caller keeps it
       if (V && t.col_wg == 0) store8(V + at, v);
@@ -318,7 +327,7 @@ __device__ __forceinline__ void stage_v(const SpreadTile& t, int n, const float*
     u32x4 o[3];
     split8(v, o);
     u32x4(*to)[64] = vop[row / 16][r8 / 4];
-    const int at = 16 * (r8 & 3) + (row & 15);
+    const int at = spread_slot<RT>(r8 / 4, r8 & 3, row & 15);
     if constexpr (RT == 1) {
       to[0][at] = o[0];
       to[0][at + 32] = o[1];
@@ -433,7 +442,7 @@ __device__ __forceinline__ void spread_columns(const SpreadTile& t, int n, int d
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int m = 0; m < TERMS; ++m) {
-          const u32x4 v = vop[i][ks][m][lane];
+          const u32x4 v = vop[i][ks][m][spread_slot<RT>(ks, g, j)];
 #pragma unroll
           for (int q = 0; q < CW; ++q) acc[q] = mfma(v, w[ks][q], acc[q]);
         }
