@@ -515,17 +515,17 @@ int low_tiles(int n, int nseg, int rmax) {
 bool short_requests(int n, int nseg) { return n / nseg <= 16; }
 
 // Workgroups along k: three for every compute unit over the whole grid, in one
-// round, while each of their waves still has a piece of 64 values of its own.
-// Whoever reads V adds their parts up, at most nine for short requests (4096 in:
-// one token 7.9 against 8.7 us with 16, both kernels) and 16 for long ones.
+// round (16384 x 5120, rank 64: 42 us in two parts, 48 in five, 57 in one).  Not
+// more than the root of the pieces that k has for them, since every workgroup
+// that reads V adds their parts up (low and spread kernel together: one token of
+// 4096 in 4 parts 7.8 us, in 9 parts 8.5; 4096 x 12288 at rank 32 in 7 parts 49.6
+// us, in 11 parts 51.8, in 3 parts 50.5).
 int low_splits(int n, int d, int nseg, int rmax) {
-  const int tt = low_tiles(n, nseg, rmax);
-  const int64_t tiles = tile_numbers(n, 16 * tt, nseg);
-  const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves), most = tt == 1 ? 9 : 16;
-  int s = static_cast<int>(768 / tiles);
-  if (s > most) s = most;
-  if (s > pieces) s = pieces;
-  return s < 1 ? 1 : s;
+  const int64_t tiles = tile_numbers(n, 16 * low_tiles(n, nseg, rmax), nseg);
+  const int pieces = (d + 64 * kWaves - 1) / (64 * kWaves);
+  int s = static_cast<int>(768 / tiles), most = 1;
+  while (most < s && most * most < pieces) ++most;
+  return s < 1 ? 1 : most;
 }
 
 template <class X, int RT>
