@@ -18,6 +18,11 @@
 // neighbouring lanes, and its maximum takes two or three DPP steps.  Results
 // that a later pass reads are written past the caches where they are larger
 // than those (non-temporal stores).
+//
+// Gated activation on 16384 x 17408, fp32 in, bf16 and both checkpoints out: 597
+// us, 5.8 TB/s; its backward, bf16 in, fp32 out: 581 us, 5.9 TB/s.  A copy of 1
+// GiB moves 5.0 TB/s here.  Storing 4099 x 5120 in bf16 takes 12 us and reading
+// back 12 us, 5.3 TB/s.
 
 #include <hip/hip_runtime.h>
 
@@ -182,7 +187,10 @@ __device__ __forceinline__ void get_codes(int64_t row, int col, int d, const uin
   c.byte = scales[row * (d / 32) + col / 32];
 }
 
-// Values per run: see the top.
+// Values per run: eight bf16 values or four fp32 ones fill a lane's 16 bytes.
+// Eight fp32 values a lane, two accesses that each skip every other 16 bytes,
+// took 1272 instead of 1226 us on 16384 x 17408, forward and backward, with all
+// outputs through the caches.
 template <class A, class B>
 constexpr int run_of = is_f32<A> || is_f32<B> ? 4 : 8;
 
@@ -296,7 +304,8 @@ __global__ __launch_bounds__(64 * kWaves) void act8_swiglu_bwd_kernel(
 int per_row(int d) { return (d + 511) / 512; }
 
 // Whether an output of n x d values passes the 256 MB of the last-level cache:
-// then it is written past the caches, which keeps them for the inputs.
+// then it is written past the caches, which keeps them for the inputs (16384 x
+// 17408, forward and backward: 1183 against 1226 us).
 bool past(int n, int d, wush_dtype t) {
   return static_cast<int64_t>(n) * d * (t == WUSH_F32 ? 4 : 2) > (int64_t{256} << 20);
 }

@@ -126,8 +126,10 @@ __device__ __forceinline__ int lane_prefix(int v) {   // inclusive
   return v;
 }
 
-// Steps of a chunk at least, and the relative cost of a step: what the rows
-// take, and the products of each row tile.
+// Steps of a chunk at least, so that its start and its part of the join stay
+// small beside it (it matters only to short calls), and the relative cost of a
+// step: what the rows take, and the products of each row tile (16384 tokens, four
+// adapters of rank 8 to 64, act8 X: 85 us, with all steps taken as equal 94).
 constexpr int kMinSteps = 4;
 __device__ __forceinline__ float step_cost(int rank, int rmax) {
   const int tiles = (min(max(rank, 1), rmax) + 15) / 16;

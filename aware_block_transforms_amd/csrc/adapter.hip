@@ -10,11 +10,12 @@
 //   low     V  = alpha X A^T   (also dV from dY and Bt)
 //   spread  Y  = Y0 + V Bt     (also dX from dV and A)
 //   grad    dA = dV^T X        (also dBt from V and dY), in adapter_grad.hip
-// All are bound by HBM at ranks up to 64: a rank-r pass does r flops per byte
-// of X, against a matrix rate of some 300 per byte of bandwidth.  So X, Y0, Y
-// and dY stream once, straight from memory into matrix operands, and the
-// operands of fp32 values are split into three bf16 terms (split3), which
-// keeps V and all results at fp32 accuracy.
+// All are bound by memory at ranks up to 64: a pass over bf16 rows at rank r does
+// r flops per byte of them, against a matrix rate of some 230 per byte that a
+// large copy moves.  So X, Y0, Y and dY are read once by each kernel, and the
+// operands of fp32 values are split into three bf16 terms (split3), which keeps V
+// and all results at fp32 accuracy.  dY is read twice by a backward call, by the
+// low and the grad kernel: dBt needs V of all tokens, dV a whole row of dY.
 
 #include <hip/hip_runtime.h>
 
@@ -55,6 +56,11 @@ constexpr int kWaves = 4;
 // piece is on its way, in registers, during the products of the one in LDS; no
 // barrier is needed.  Rows past the tile's tokens or the rank, and columns past
 // d, lie outside the buffer resources and come as zeros.
+//
+// 16384 x 5120 in bf16 at rank 64: 42 us, 4.0 TB/s of X (55 us with operands
+// loaded row by row); 4096 x 12288 at rank 32: 28 us, 3.7 TB/s.  Waits for loads
+// are what is left: two pieces ahead in registers were slower (88 us, they cost
+// half of the waves), and so were other orders of k.
 
 // A piece of 64 columns of 16 N rows: C 16-byte chunks a row.
 template <class T, int N>
@@ -240,6 +246,13 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
 // column: the workgroup adds up the low kernel's parts and splits them once,
 // into LDS, in the order the matrix instructions take them.  The sums start
 // from Y0, whose next rows are loaded before the products of those in hand.
+//
+// 16384 x 17408 in fp32 at rank 64: 393 us, 5.8 TB/s of Y0 and Y, what a copy of
+// that size reaches or more.  64 requests of one token on 12288 columns: 14 us,
+// which the start of a workgroup (its request, the parts of V, the first factor
+// rows) and five column blocks in turn take.  More and shorter workgroups do not
+// help (16 us with 1152, 23 us with 3264, against 704), nor does an order that
+// keeps requests of one column block on one XCD.
 
 template <class T>
 struct YRow;
@@ -460,7 +473,7 @@ __device__ __forceinline__ void spread_columns(const SpreadTile& t, int n, int d
 }
 
 // Short requests live on the number of waves: three a SIMD, where the factor's
-// operands leave the registers for it (64 requests on 12288 columns: 14.6 against 16.5 us).
+// operands leave the registers for it (64 requests on 12288 columns: 13.6 against 16.5 us).
 template <class Y, int RT, int TT, bool BASE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves, TT == 1 && RT * YRow<Y>::CW <= 16 ? 3 : 1) void adapter_spread_kernel(int n, int d, int col_wgs,
                                                                      const float* __restrict__ part, int splits,
@@ -502,7 +515,9 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(int64_t count, const f
 
 // Token tiles of the low kernel: as many rows as the average request fills, so
 // that the factor's rows are read once for them; at most 64, 32 at rank 128
-// (the sums take 64 registers per lane at either limit).
+// (the sums take 64 registers per lane at either limit).  16384 x 5120 at rank
+// 64: 42 us with 64 rows, 58 with 32 or 16; 4096 x 12288 at rank 32: 27 us with
+// 64, 29 with 32, 37 with 16.
 int low_tiles(int n, int nseg, int rmax) {
   const int avg = n / (nseg > 0 ? nseg : 1);
   const int most = rmax > 64 ? 2 : 4;
@@ -511,7 +526,8 @@ int low_tiles(int n, int nseg, int rmax) {
 }
 
 // Tokens a spread workgroup walks over: 64, so that the factor's operands are
-// built once for four tiles; 16 where requests are short.
+// built once for four tiles (16384 x 17408: 393 us, with 16 tokens 519); 16 where
+// requests are short (64 of one token on 12288 columns: 14 us, with 64 tokens 19).
 bool short_requests(int n, int nseg) { return n / nseg <= 16; }
 
 // Workgroups along k: three for every compute unit over the whole grid, in one
@@ -561,7 +577,7 @@ void spread_by_tiles(bool one, int n, int d, const float* part, int splits, int 
   const int col_wgs = one && few < all ? few : all;
   const dim3 grid(static_cast<unsigned>(col_wgs * tiles));
   // Y beyond the 256 MB of the last-level cache goes past the caches, which keep
-  // the inputs of the next call instead (16384 x 17408 fp32: 449 against 463 us
+  // the inputs of the next call instead (16384 x 17408 fp32: 437 against 459 us
   // for both kernels)
   const bool far = static_cast<int64_t>(n) * d * static_cast<int64_t>(sizeof(Y)) > (int64_t{256} << 20);
   auto k = one ? (y0 ? adapter_spread_kernel<Y, RT, 1, true, false> : adapter_spread_kernel<Y, RT, 1, false, false>)

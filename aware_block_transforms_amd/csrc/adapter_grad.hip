@@ -17,6 +17,12 @@
 // and share the operands of S, which they split into three bf16 terms together,
 // one step ahead, through two LDS buffers.  The rows of X are loaded one step
 // ahead too, into the registers that the step's operands have just left.
+//
+// Bound by the loads' latency at two waves a SIMD, whose accumulators (16 RT x
+// 128 fp32 a wave) leave no room for more.  4096 tokens, 4096 + 12288 bf16
+// columns at rank 32: 30 us and 6.5 us of join, 4.5 TB/s of X and dY.  16384
+// tokens, 17408 act8 + 5120 bf16 columns at rank 64: 85 us and 11 us, 5.4 TB/s
+// (each wave splitting all of S by itself: 147 us).
 
 #include <hip/hip_runtime.h>
 
@@ -323,7 +329,8 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(Side a, Side b, int R
 
 // Chunks wanted: so many that the workgroups fit the compute units once (two on
 // each; three at rank 16, one at rank 128), since a second round for the last
-// few would take as long as the first.
+// few would take as long as the first.  With the join, the two cases above take
+// 36 and 96 us; 45 and 162 with half as many, 49 and 107 with twice as many.
 int chunks_wanted(int n, int d_in, int d_out, int rmax) {
   const int wgs = (d_in + kCols - 1) / kCols + (d_out + kCols - 1) / kCols;
   const int slots = rmax == 16 ? 768 : rmax == 128 ? 256 : 512;

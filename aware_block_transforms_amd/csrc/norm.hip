@@ -14,7 +14,11 @@
 //   p  = g gate w_post,          dY = k1 (p - z mean(p z)),        dR = res t
 // All sums are fp32.
 //
-// Both directions are bound by HBM: every value is read and written once.  A
+// Both directions are bound by HBM: every value is read and written once.
+// Forward on 16384 x 5120, y fp32, the rest bf16: 151 us, 5.5 TB/s.  Backward on
+// 4096 x 4096: 51 us and 4 us for the column sums, 4.9 TB/s; a copy of 256 MB
+// moves 5.4 TB/s here, one of 1 GiB 5.0.  One row of 4096 takes 3.2 us, a turn
+// through memory for the loads, one for the weights, and the launch.  A
 // workgroup owns a row, a thread VPT pieces of eight values of it, which stay
 // in registers between the two means.  In the backward kernel a workgroup
 // walks over rows and keeps its columns' weight gradients in registers; the
@@ -177,7 +181,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
 // (zero past the last column, which also drops what the threads there add to a
 // sum; they read the last columns again), the two rsqrt values come through the
 // scalar cache, and tensors that the caller left out are read as one that is
-// there and replaced by zeros, not skipped by a branch.
+// there and replaced by zeros, not skipped by a branch.  Where a branch or
+// a weight load cut the row's loads off, 4096 x 4096 took 71 us against 59 with
+// as many workgroups.
 template <class Y, class R, class U, int MAXT, int GATE>
 __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float* __restrict__ k1s,
                                                         const float* __restrict__ k2s, const U* __restrict__ du,
@@ -580,6 +586,7 @@ extern "C" wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtyp
     using UT = decltype(u);
     const int vpt = fwd_vpt(n, d);
     // outputs beyond the 256 MB of the last-level cache are written past it
+    // (16384 x 5120, both in bf16: 150 against 157 us)
     const int64_t out = static_cast<int64_t>(n) * d * ((Rout ? sizeof(RT) : 0) + (U ? sizeof(UT) : 0));
     const bool far = out > (int64_t{256} << 20);
     auto k = vpt == 1   ? norm_fwd_kernel<YT, RT, UT, 1, false>
