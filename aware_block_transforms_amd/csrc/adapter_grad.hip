@@ -20,9 +20,12 @@
 //
 // Bound by the loads' latency at two waves a SIMD, whose accumulators (16 RT x
 // 128 fp32 a wave) leave no room for more.  4096 tokens, 4096 + 12288 bf16
-// columns at rank 32: 30 us and 6.5 us of join, 4.5 TB/s of X and dY.  16384
-// tokens, 17408 act8 + 5120 bf16 columns at rank 64: 85 us and 11 us, 5.4 TB/s
-// (each wave splitting all of S by itself: 147 us).
+// columns at rank 32: 30 us and 6.5 us of join, 5.6 TB/s with the parts.  16384
+// tokens, 17408 act8 + 5120 bf16 columns at rank 64, 70% of the tokens with an
+// adapter: 86 us and 11 us, 4.4 TB/s; the matrix cores are busy for 22 us of it,
+// turning codes into values takes as long (each wave splitting all of S by
+// itself: 147 us).  An order of the workgroups that keeps a chunk's columns on
+// one XCD reads S once but takes 96 us.
 
 #include <hip/hip_runtime.h>
 
