@@ -310,10 +310,10 @@ bool past(int n, int d, wush_dtype t) {
   return static_cast<int64_t>(n) * d * (t == WUSH_F32 ? 4 : 2) > (int64_t{256} << 20);
 }
 
-// Workgroups of n rows, 0 if they pass the launch limit.
+// Workgroups of n rows, 0 if they pass the launch limit of 2^32 threads.
 unsigned blocks(int n, int d) {
   const int64_t b = (static_cast<int64_t>(n) * per_row(d) + kWaves - 1) / kWaves;
-  return b <= 0x7fffffff ? static_cast<unsigned>(b) : 0u;
+  return b < (int64_t{1} << 32) / (64 * kWaves) ? static_cast<unsigned>(b) : 0u;
 }
 
 wush_status check(const char* who, wush_dtype a, wush_dtype b, int n, int d) {

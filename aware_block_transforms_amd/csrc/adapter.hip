@@ -632,8 +632,9 @@ wush_status check(const char* who, wush_dtype a, wush_dtype b, wush_dtype c, int
   if (!rank_ok(rmax)) return fail(WUSH_E_SHAPE, "%s: rmax must be 16, 32, 64 or 128 (got %d)", who, rmax);
   if (nad < 1 || nseg < 1 || nseg > kMaxSeg)
     return fail(WUSH_E_SHAPE, "%s: need at least one adapter and 1..%d requests (nad=%d nseg=%d)", who, kMaxSeg, nad, nseg);
+  // short requests launch no more workgroups than they have tiles (or 768)
   const int64_t d = d_in > d_out ? d_in : d_out;
-  if ((tile_numbers(n, short_requests(n, nseg) ? 16 : 64, nseg) + 7) * ((d + 255) / 256) > 0x7fffffff)
+  if (!short_requests(n, nseg) && (tile_numbers(n, 64, nseg) + 7) * ((d + 255) / 256) >= (int64_t{1} << 32) / (64 * kWaves))
     return fail(WUSH_E_SHAPE, "%s: n=%d with nseg=%d passes the launch limit", who, n, nseg);
   return WUSH_OK;
 }

@@ -572,6 +572,8 @@ extern "C" wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtyp
   if (st != WUSH_OK) return st;
   if (!(eps > 0.0f) || !__builtin_isfinite(eps)) return fail(WUSH_E_ARG, "%s: eps must be positive and finite", who);
   if (n == 0) return WUSH_OK;
+  if (static_cast<int64_t>(n) * threads(d, fwd_vpt(n, d)) >= int64_t{1} << 32)
+    return fail(WUSH_E_SHAPE, "%s: n=%d d=%d passes the launch limit", who, n, d);
   if ((w_pre != nullptr) != (U != nullptr)) return fail(WUSH_E_ARG, "%s: w_pre and U are given together", who);
   if (!R || (!U && !Rout)) return fail(WUSH_E_ARG, "%s: null pointer", who);
   for (const void* p : {Y, static_cast<const void*>(w_post), R, static_cast<const void*>(w_pre),

@@ -434,7 +434,8 @@ typedef enum {
  *           the input of wush_transform_quant.
  *   rstd_post, rstd_pre  device out, fp32 [n]: the two rsqrt values, which the
  *           backward call needs; or NULL.
- * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0; d not a multiple of 8 in 8..24576),
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0; d not a multiple of 8 in 8..24576; so
+ * many rows, 2^22 or more by d, that one launch does not hold them),
  * WUSH_E_UNSUPPORTED (udt), WUSH_E_HIP. */
 wush_status wush_block_norm(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, int n, int d,
                             const void* Y, const float* w_post, wush_gate gate_kind,
@@ -468,7 +469,8 @@ wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, 
  * A group with a NaN or an infinity gets byte 0xFF and zero codes, and stands
  * for NaN.  Every value is a bf16 number.
  *   codes   device, [n][d] int8, 16-byte aligned.   scales  device, [n][d/32] bytes.
- * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0, d % 32), WUSH_E_HIP. */
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0, d % 32, rows of 2^26 or more
+ * pieces of 512 values in all: the launch limit), WUSH_E_HIP. */
 wush_status wush_act8_pack(wush_dtype xdt, int n, int d, const void* X, int8_t* codes,
                            uint8_t* scales, void* stream);
 wush_status wush_act8_unpack(wush_dtype ydt, int n, int d, const int8_t* codes,

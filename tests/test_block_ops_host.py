@@ -133,6 +133,15 @@ def test_adapter_backward_refusals(kw, status):
     assert L.wush_last_error().startswith(b"wush_adapter_backward:")
 
 
+def test_calls_past_the_launch_limit_are_refused():
+    # 2^32 threads: a row of the norm has at least 64, 512 values of act8 have 64, 64 x 256 values of Y have 256
+    assert norm(n=1 << 26) == W.WUSH_E_SHAPE and b"launch limit" in L.wush_last_error()
+    assert L.wush_act8_pack(0, 1 << 26, 512, P, P, P, None) == W.WUSH_E_SHAPE and b"launch limit" in L.wush_last_error()
+    wide = 1 << 22
+    assert adapter(n=1 << 24, nseg=1, d_out=wide, ldy=wide, ldy0=wide) == W.WUSH_E_SHAPE
+    assert b"launch limit" in L.wush_last_error()
+
+
 def test_workspace_sizes_of_bad_shapes_are_zero():
     assert L.wush_block_norm_bwd_ws_bytes(0, 64) == 0 and L.wush_block_norm_bwd_ws_bytes(4, 12) == 0
     assert L.wush_block_norm_bwd_ws_bytes(1, 64) >= 3 * 64 * 4
