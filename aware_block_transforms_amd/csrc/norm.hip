@@ -177,13 +177,14 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
 // Partial column sums of one workgroup: [3][d] (dw_pre, dw_post, dgate).  A
 // thread owns eight columns of rows up to 8 MAXT.  The next row is loaded, into
 // a second buffer, before the sums over the one in hand.  Loads return in order,
-// so nothing may be loaded and waited for in between: the weights lie in LDS
-// (zero past the last column, which also drops what the threads there add to a
-// sum; they read the last columns again), the two rsqrt values come through the
-// scalar cache, and tensors that the caller left out are read as one that is
-// there and replaced by zeros, not skipped by a branch.  Where a branch or
-// a weight load cut the row's loads off, 4096 x 4096 took 71 us against 59 with
-// as many workgroups.
+// so nothing may be loaded and waited for in between: the weights lie in LDS,
+// the two rsqrt values come through the scalar cache, threads past the last
+// column read the last columns again, and tensors that the caller left out are
+// read as one that is there and replaced by zeros, not skipped by a branch.
+// Where a branch or a weight load cut the row's loads off, 4096 x 4096 took 71 us
+// against 59 with as many workgroups.  What the threads past the last column
+// would add to a row's sums is dropped by a select on the sum: a factor of zero
+// would make NaN of a row whose gradient holds an infinity there.
 template <class Y, class R, class U, int MAXT, int GATE>
 __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float* __restrict__ k1s,
                                                         const float* __restrict__ k2s, const U* __restrict__ du,
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float*
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       w[h] = from ? reinterpret_cast<const f32x4*>(from + col)[h] : f32x4{otherwise, otherwise, otherwise, otherwise};
-      weights[which][me][h] = in ? w[h] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      weights[which][me][h] = w[h];
     }
   };
   keep(0, a.w_pre, 0.0f);
@@ -247,6 +248,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float*
       q[i] *= w[i];
       m = __builtin_fmaf(q[i], x[i], m);
     }
+    m = in ? m : 0.0f;
     block_sums<1>(&m, slots[0]);
     m *= inv_d;
     float t[8], z[8], g[8], o[8], sums[2] = {0.0f, 0.0f};   // p z, and the token gate's gradient
@@ -284,6 +286,8 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float*
     }
     if constexpr (ELEMENT)
       if (in) store8(static_cast<Y*>(dgate) + at, o);
+    sums[0] = in ? sums[0] : 0.0f;
+    sums[1] = in ? sums[1] : 0.0f;
     block_sums<2>(sums, slots[1]);
     if (GATE == WUSH_GATE_TOKEN && dgate && me == 0) static_cast<float*>(dgate)[row] = sums[1];
     // without a norm after the block dY is p itself

@@ -1,0 +1,59 @@
+"""Block norm, act8 and adapters on the GPU at their edges: infinities, wide rows in numbers, many adapters, outputs
+beyond the last-level cache, streams and graphs.
+
+Bounds are those of test_gpu_block_ops: (K + 32) 2^-24 times the result computed from magnitudes, and 2^-8 of its value
+for bf16 results.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import aware_block_transforms_amd as W
+from oracle import block_ops as bo
+from gpu_util import DEV
+from test_gpu_block_ops import _norm_inputs, dev, f64, new
+
+pytestmark = pytest.mark.gpu
+
+
+def same_kind(got, ref):
+    """NaN where the definition has NaN, and its infinities."""
+    g = f64(got)
+    return np.array_equal(np.isnan(g), np.isnan(ref)) and np.array_equal(np.where(np.isinf(g), g, 0),
+                                                                        np.where(np.isinf(ref), ref, 0))
+
+
+# ----------------------------------------------------------------------------- block norm
+
+
+@pytest.mark.parametrize("d", [264, 512, 520, 2600, 4104])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "element"])
+def test_norm_gradient_of_an_infinity_in_the_last_column(gate, d):
+    # the row's gradients are the definition's, infinite or NaN, whether or not threads lie past the last column; the
+    # other rows stay as they were
+    n, types = 3, ("f32", "f32", "f32")
+    r, Y, wp, g, R, w = _norm_inputs(101, n, d, types, gate)
+    Y[1], R[2] = dev(r.standard_normal(d)), dev(r.standard_normal(d))
+    Rout, U, k1, k2 = new(n, d), new(n, d), new(n), new(n)
+    W.wush_block_norm(Y, wp, g, R, w, Rout, U, k1, k2)
+
+    def grads(dU, dRo):
+        dY, dR, dg, dwp, dw = new(n, d), new(n, d), None if g is None else torch.full_like(g, 7.0), new(d), new(d)
+        W.wush_block_norm_bwd(dU, dRo, Y, wp, g, Rout, w, k1, k2, dY, dR, dg, dwp, dw)
+        torch.cuda.synchronize()
+        return dY, dR, dg
+    clean = [dev(r.standard_normal((n, d))) for _ in range(2)]
+    want = grads(*clean)
+    for which in (0, 1):
+        bad = [t.clone() for t in clean]
+        bad[which][1, d - 1] = float("inf")
+        dY, dR, dg = grads(*bad)
+        for t, o in zip((dY, dR), want):
+            assert torch.equal(t[[0, 2]], o[[0, 2]])
+        with np.errstate(invalid="ignore"):
+            ref = bo.block_norm_bwd(f64(bad[0]), f64(bad[1]), f64(Y), f64(wp), f64(g), f64(Rout), f64(w), f64(k1),
+                                    f64(k2), 1.0, 1.0)
+            row = {"token": ref["dgate"].sum(1, keepdims=True), "channel": ref["dgate"].sum(0)}.get(gate, ref["dgate"])
+        assert same_kind(dR, ref["dR"]) and same_kind(dY, ref["dY"])
+        assert g is None or same_kind(dg, row)
