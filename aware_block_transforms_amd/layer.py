@@ -95,11 +95,18 @@ def request_table(lengths, adapters, device="cuda"):
     return torch.from_numpy(off).to(device), torch.tensor(adapters, dtype=torch.int32, device=device)
 
 
+def _scratch(need, device):
+    """A call's workspace.  It belongs to the call alone: torch's allocator takes it from the current stream's blocks, or
+    from the pool of the graph being captured, so calls on several streams, and replays, never meet in one."""
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
 class AdapterSet:
-    """Low-rank adapters beside one projection d_in -> d_out, and their workspaces.
+    """Low-rank adapters beside one projection d_in -> d_out.
 
     ``A`` [nad][rmax][d_in] and ``Bt`` [nad][rmax][d_out] are bfloat16 (Bt is the transpose of the usual B and starts at
-    zero), ``rank`` and ``alpha`` per adapter.  A request table (see ``request_table``) says whose tokens are whose.
+    zero), ``rank`` and ``alpha`` per adapter.  A request table (see ``request_table``) says whose tokens are whose.  Calls
+    run on the current stream and keep nothing in the set: one set serves several streams and captured graphs at a time.
     """
 
     def __init__(self, nad, rmax, d_in, d_out, rank=None, alpha=1.0, device="cuda", seed=0):
@@ -111,12 +118,6 @@ class AdapterSet:
         self.rank = torch.tensor([rmax] * nad if rank is None else list(rank), dtype=torch.int32, device=device)
         self.alpha = torch.tensor([float(alpha)] * nad if np.isscalar(alpha) else list(alpha), dtype=torch.float32,
                                   device=device)
-        self._ws = None   # grown on demand
-
-    def _scratch(self, need, device):
-        if self._ws is None or self._ws.numel() < need or self._ws.device != device:
-            self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        return self._ws
 
     def forward(self, X, requests, Y0, out=None, keep=False):
         """Y = Y0 + alpha X A^T Bt, per request; with ``keep`` also V, which the backward pass needs."""
@@ -124,7 +125,7 @@ class AdapterSet:
         n = X.shape[0]
         Y = out if out is not None else torch.empty_like(Y0)
         V = torch.empty((n, self.rmax), dtype=torch.float32, device=X.device) if keep else None
-        ws = self._scratch(W.wush_adapter_ws_bytes(n, self.d_in, ids.shape[0], self.rmax), X.device)
+        ws = _scratch(W.wush_adapter_ws_bytes(n, self.d_in, ids.shape[0], self.rmax), X.device)
         W.wush_adapter_forward(X, off, ids, self.A, self.Bt, self.rank, self.alpha, Y0, Y, V=V, ws=ws)
         return (Y, V) if keep else Y
 
@@ -135,8 +136,7 @@ class AdapterSet:
         dX = torch.empty((n, self.d_in), dtype=dx_dtype if dX0 is None else dX0.dtype, device=dev)
         dA = torch.empty((self.nad, self.rmax, self.d_in), dtype=torch.float32, device=dev)
         dBt = torch.empty((self.nad, self.rmax, self.d_out), dtype=torch.float32, device=dev)
-        ws = self._scratch(W.wush_adapter_backward_ws_bytes(n, self.d_in, self.d_out, ids.shape[0], self.nad, self.rmax),
-                           dev)
+        ws = _scratch(W.wush_adapter_backward_ws_bytes(n, self.d_in, self.d_out, ids.shape[0], self.nad, self.rmax), dev)
         W.wush_adapter_backward(dY, X, off, ids, self.A, self.Bt, self.rank, self.alpha, V, dX0, dX, dA, dBt,
                                 x_scales=x_scales, ws=ws)
         return dX, dA, dBt

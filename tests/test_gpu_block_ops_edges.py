@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import aware_block_transforms_amd as W
+from aware_block_transforms_amd.layer import AdapterSet, request_table
 from oracle import block_ops as bo
 from gpu_util import DEV
 from test_gpu_block_ops import _norm_inputs, dev, f64, new
@@ -57,3 +58,66 @@ def test_norm_gradient_of_an_infinity_in_the_last_column(gate, d):
             row = {"token": ref["dgate"].sum(1, keepdims=True), "channel": ref["dgate"].sum(0)}.get(gate, ref["dgate"])
         assert same_kind(dR, ref["dR"]) and same_kind(dY, ref["dY"])
         assert g is None or same_kind(dg, row)
+
+
+# ----------------------------------------------------------------------------- streams and graphs
+
+
+def _adapter_set(seed, d_in, d_out, nad=3, rmax=32):
+    ad = AdapterSet(nad, rmax, d_in, d_out, rank=[rmax, 7, rmax // 2][:nad], alpha=[1.0, -0.5, 2.0][:nad], seed=seed)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    ad.Bt.copy_(torch.randn(ad.Bt.shape, generator=g, device=DEV) * 0.1)
+
+    def batch(lengths, ids):
+        n = sum(lengths)
+        rand = lambda d: torch.randn((n, d), generator=g, device=DEV)  # noqa: E731
+        return rand(d_in).to(torch.bfloat16), request_table(lengths, ids), rand(d_out), rand(d_out).to(torch.bfloat16)
+    return ad, batch
+
+
+def _pass(ad, b):
+    X, req, Y0, dY = b
+    Y, V = ad.forward(X, req, Y0, keep=True)
+    return (Y, V) + ad.backward(dY, X, req, V)
+
+
+def test_one_adapter_set_on_two_streams():
+    ad, batch = _adapter_set(201, 4096, 2048)
+    work = [batch([300, 0, 500, 17], [0, 1, 2, -1]), batch([1] * 40, [0, 1, 2, -1] * 10)]
+    want = [_pass(ad, b) for b in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = []
+    for turn in range(10):
+        for s, b in zip(streams, work):
+            with torch.cuda.stream(s):
+                got.append(_pass(ad, b))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2])), i
+
+
+def test_graph_of_an_adapter_set_outlives_longer_calls():
+    ad, batch = _adapter_set(202, 1024, 512)
+    small, large = batch([1] * 8, [0, 1, 2, -1] * 2), batch([900, 300, 1300], [2, 0, 1])
+    want, want_large = _pass(ad, small), _pass(ad, large)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _pass(ad, small)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _pass(ad, small)
+    for turn in range(4):
+        got = _pass(ad, large)
+        # blocks of every size that a workspace given back could be handed out as
+        canaries = [torch.full((1 << k,), turn, dtype=torch.uint8, device=DEV) for k in range(9, 24)]
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
+        assert all(torch.equal(a, b) for a, b in zip(got, want_large)), turn
+        assert all((c == turn).all() for c in canaries), turn
