@@ -21,6 +21,12 @@ def scales_dtype(fmt):
     return torch.int16 if fmt == "int4" else torch.uint8
 
 
+def _scratch(need, device):
+    """A call's workspace.  It belongs to the call alone: torch's allocator takes it from the current stream's blocks, or
+    from the pool of the graph being captured, so calls on several streams, and replays, never meet in one."""
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
 class W4A4Layer:
     """Weights Wt [d_out][d_in] (nn.Linear layout) quantized with a per-block transform."""
 
@@ -52,7 +58,6 @@ class W4A4Layer:
         self.w_g = W.wush_pack_weights(fmt, Wd, self.Tw, self.w_codes, self.w_scales)
         del Wd
         self.x_g = 1.0
-        self._ws = None   # GEMM workspace, grown on demand
 
     def calibrate(self, X):
         """NVFP4 only: per-tensor activation scale from calibration activations (device tensor)."""
@@ -71,10 +76,8 @@ class W4A4Layer:
     def matmul(self, codes, scales, Y):
         n = codes.shape[0]
         need = W.wush_w4a4_gemm_ws_bytes(self.fmt, n, self.d_out, self.d_in)
-        if need and (self._ws is None or self._ws.numel() < need or self._ws.device != codes.device):
-            self._ws = torch.empty(need, dtype=torch.uint8, device=codes.device)
         W.wush_w4a4_gemm(self.fmt, codes, scales, self.w_codes, self.w_scales, Y, a_g=self.x_g, b_g=self.w_g,
-                         ws=self._ws if need else None)
+                         ws=_scratch(need, codes.device) if need else None)
 
     def forward(self, X, out=None, adapters=None, requests=None):
         """X W^T from the quantized operands; with an AdapterSet and the requests that X is made of, their adapters
@@ -93,12 +96,6 @@ def request_table(lengths, adapters, device="cuda"):
     """(offsets, adapter ids) on the device: request i has lengths[i] tokens and adapter adapters[i], -1 for none."""
     off = np.concatenate(([0], np.cumsum(np.asarray(lengths, np.int64)))).astype(np.int32)
     return torch.from_numpy(off).to(device), torch.tensor(adapters, dtype=torch.int32, device=device)
-
-
-def _scratch(need, device):
-    """A call's workspace.  It belongs to the call alone: torch's allocator takes it from the current stream's blocks, or
-    from the pool of the graph being captured, so calls on several streams, and replays, never meet in one."""
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 
 class AdapterSet:

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import aware_block_transforms_amd as W
-from aware_block_transforms_amd.layer import AdapterSet, request_table
+from aware_block_transforms_amd.layer import AdapterSet, W4A4Layer, request_table
 from oracle import block_ops as bo
 from gpu_util import DEV
 from test_gpu_block_ops import _norm_inputs, dev, f64, new
@@ -120,4 +120,33 @@ def test_graph_of_an_adapter_set_outlives_longer_calls():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
         assert all(torch.equal(a, b) for a, b in zip(got, want_large)), turn
+        assert all((c == turn).all() for c in canaries), turn
+
+
+def test_one_layer_with_adapters_on_two_streams_and_in_a_graph():
+    ad, batch = _adapter_set(203, 1024, 512)
+    Wt = (np.random.default_rng(203).standard_normal((512, 1024)) / 32).astype(np.float32)
+    L = W4A4Layer("mxfp4", "hadamard", Wt)
+    work = [batch([30, 0, 200, 17], [0, 1, 2, -1])[:2], batch([1] * 40, [0, 1, 2, -1] * 10)[:2]]
+    want = [L.forward(X, adapters=ad, requests=req) for X, req in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = []
+    for turn in range(10):
+        for s, (X, req) in zip(streams, work):
+            with torch.cuda.stream(s):
+                got.append(L.forward(X, adapters=ad, requests=req))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))
+    (X, req), (X2, req2) = work[1], work[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = L.forward(X, adapters=ad, requests=req)
+    for turn in range(4):
+        large = L.forward(X2, adapters=ad, requests=req2)
+        canaries = [torch.full((1 << k,), turn, dtype=torch.uint8, device=DEV) for k in range(9, 22)]
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[1]) and torch.equal(large, want[0]), turn
         assert all((c == turn).all() for c in canaries), turn

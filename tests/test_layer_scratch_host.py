@@ -24,3 +24,16 @@ def test_calls_of_one_adapter_set_share_no_workspace(monkeypatch):
             layer.W.wush_adapter_ws_bytes(n, d_in, nseg, rmax)
         assert t.numel() >= need
     assert not any(torch.is_tensor(v) and v.data_ptr() in {t.data_ptr() for t in held} for v in vars(ad).values())
+
+
+def test_calls_of_one_layer_share_no_workspace(monkeypatch):
+    held = []
+    monkeypatch.setattr(layer.W, "wush_w4a4_gemm", lambda *a, ws, **k: held.append(ws))
+    L = object.__new__(layer.W4A4Layer)          # packing weights needs a GPU
+    vars(L).update(fmt="mxfp4", bs=32, d_in=256, d_out=128, x_g=1.0, w_g=1.0, w_codes=None, w_scales=None)
+    codes, scales = L.alloc_activation_codes(64, "cpu")
+    for _ in range(3):
+        L.matmul(codes, scales, torch.zeros(64, 128))
+    need = layer.W.wush_w4a4_gemm_ws_bytes("mxfp4", 64, 128, 256)
+    assert need > 0 and all(t.numel() >= need for t in held)
+    assert len(held) == 3 and len({t.data_ptr() for t in held}) == 3
