@@ -630,7 +630,8 @@ extern "C" wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   for (const void* p : {dU, dRout, Y, static_cast<const void*>(w_post), Rout, static_cast<const void*>(w_pre),
-                        static_cast<const void*>(dY), static_cast<const void*>(dR), static_cast<const void*>(ws)})
+                        static_cast<const void*>(dY), static_cast<const void*>(dR), static_cast<const void*>(dw_post),
+                        static_cast<const void*>(dw_pre), static_cast<const void*>(ws)})
     if (!aligned16(p)) return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
   if ((!aligned16(gate) || !aligned16(dgate)) && gate_kind != WUSH_GATE_TOKEN)
     return fail(WUSH_E_ARG, "%s: pointers must be 16-byte aligned", who);
