@@ -301,6 +301,9 @@ __global__ __launch_bounds__(64 * kWaves) void act8_swiglu_bwd_kernel(
   }
 }
 
+// Columns are counted in 31 bits, to the end of a row's last piece.
+constexpr int kMaxD = 0x7fffffff - 511;
+
 int per_row(int d) { return (d + 511) / 512; }
 
 // Whether an output of n x d values passes the 256 MB of the last-level cache:
@@ -319,7 +322,8 @@ unsigned blocks(int n, int d) {
 wush_status check(const char* who, wush_dtype a, wush_dtype b, int n, int d) {
   if ((a != WUSH_F32 && a != WUSH_BF16) || (b != WUSH_F32 && b != WUSH_BF16))
     return fail(WUSH_E_ARG, "%s: bad dtype", who);
-  if (n < 0 || d < 32 || d % 32) return fail(WUSH_E_SHAPE, "%s: need n >= 0 and d a positive multiple of 32 (n=%d d=%d)", who, n, d);
+  if (n < 0 || d < 32 || d % 32 || d > kMaxD)
+    return fail(WUSH_E_SHAPE, "%s: need n >= 0 and d a multiple of 32 in 32..%d (n=%d d=%d)", who, kMaxD, n, d);
   if (n > 0 && blocks(n, d) == 0) return fail(WUSH_E_SHAPE, "%s: n=%d d=%d passes the launch limit", who, n, d);
   return WUSH_OK;
 }

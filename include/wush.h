@@ -469,8 +469,8 @@ wush_status wush_block_norm_bwd(wush_dtype ydt, wush_dtype rdt, wush_dtype udt, 
  * A group with a NaN or an infinity gets byte 0xFF and zero codes, and stands
  * for NaN.  Every value is a bf16 number.
  *   codes   device, [n][d] int8, 16-byte aligned.   scales  device, [n][d/32] bytes.
- * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0, d % 32, rows of 2^26 or more
- * pieces of 512 values in all: the launch limit), WUSH_E_HIP. */
+ * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n < 0, d % 32, d above 2^31 - 512, rows of
+ * 2^26 or more pieces of 512 values in all: the launch limit), WUSH_E_HIP. */
 wush_status wush_act8_pack(wush_dtype xdt, int n, int d, const void* X, int8_t* codes,
                            uint8_t* scales, void* stream);
 wush_status wush_act8_unpack(wush_dtype ydt, int n, int d, const int8_t* codes,

@@ -11,3 +11,14 @@ def test_block_norm_bwd_refuses_unaligned_sums(kw):
     # the column sums are written 16 bytes at a time
     assert norm_bwd(**kw) == W.WUSH_E_ARG
     assert b"16-byte aligned" in L.wush_last_error()
+
+
+@pytest.mark.parametrize("d", [2 ** 31 - 32, 2 ** 31 - 480])
+def test_act8_refuses_rows_whose_columns_pass_31_bits(d):
+    # the last piece of 512 columns of such a row ends past 2^31 - 1
+    shape = W.WUSH_E_SHAPE
+    assert L.wush_act8_pack(1, 1, d, P, P, P, None) == shape
+    assert L.wush_act8_unpack(1, 1, d, P, P, P, None) == shape
+    assert L.wush_act8_swiglu(1, 1, 1, d, P, P, d, P, P, P, P, P, None) == shape
+    assert L.wush_act8_swiglu_bwd(1, 1, 1, d, P, P, P, P, P, P, P, d, None) == shape
+    assert L.wush_act8_pack(1, 0, 2 ** 31 - 512, None, None, None, None) == W.WUSH_OK
