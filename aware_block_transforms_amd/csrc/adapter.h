@@ -136,34 +136,64 @@ __device__ __forceinline__ float step_cost(int rank, int rmax) {
   return tiles > 4 ? 9.0f : tiles > 2 ? 6.0f : tiles > 1 ? 5.0f : 4.5f;
 }
 
-// Makes the lists; one workgroup of WAVES waves.  Its passes over the requests
-// depend on each other, and each takes a turn through memory: some 9 us in all,
-// which the low kernel of the backward call hides by giving it a workgroup of
-// its own.
+// Makes the lists; one workgroup of WAVES waves, to which the low kernel of the
+// backward call gives a place beside its own.  The work grows with the requests
+// and with the adapters, not with their product: one wave goes over the requests,
+// 64 at a time, and counts the tokens of every adapter as it finds each request's
+// place among them; the lists' lengths then give the chunks, and all waves write
+// the tokens.  Few requests hide behind the low kernel.  Many do not: some 7 us
+// for each 64 requests (16384 tokens, 4096 + 4096 columns at rank 16, the whole
+// backward call: 158 us for 12 requests of 4 adapters, 173 for 128 of 32, 219 for
+// 512 of 128, 700 for 4096 of 256; with a wave that went over all requests for
+// each adapter 158, 204, 440 and 3097).
 template <int WAVES>
 __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, const int* ids, int nad, const int* rank,
                                             int rmax, int chunks_wanted, const Lists& l) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto length = [&](int s, int a) {
-    if (s >= nseg || ids[s] != a) return 0;
-    return max(request_start(off, s + 1, nseg, n) - request_start(off, s, nseg, n), 0);
-  };
-  // one wave per adapter: its tokens (none where its rank is zero)
-  for (int a = wave; a < nad; a += WAVES) {
-    int sum = 0;
-    if (rank[a] > 0)
-      for (int b = 0; b < nseg; b += 64) sum = min(sum + length(b + lane, a), n);
-    sum = __shfl(lane_prefix(sum), 63, 64);
-    if (lane == 0) l.count[a] = min(sum, n);
-  }
+  for (int a = threadIdx.x; a < nad; a += 64 * WAVES) l.count[a] = 0;
   __syncthreads();
+  // a request's adapter (-1: none), first token and tokens
+  struct Request {
+    int adapter, first, tokens;
+  };
+  auto request = [&](int s) {
+    Request r{-1, 0, 0};
+    if (s >= nseg) return r;
+    const int a = ids[s];
+    r.first = request_start(off, s, nseg, n);
+    r.tokens = max(request_start(off, s + 1, nseg, n) - r.first, 0);
+    if (a >= 0 && a < nad && r.tokens > 0) r.adapter = a;
+    return r;
+  };
   if (wave == 0) {
-    // a list's cost: its tokens times the cost of a step at its rank
+    Request next = request(lane);
+    for (int b = 0; b < nseg; b += 64) {
+      const Request r = next;
+      next = request(b + 64 + lane);
+      int at = b > 0 && r.adapter >= 0 ? l.count[r.adapter] : 0;
+      bool last = true;   // of its adapter's requests among the 64
+#pragma unroll 8
+      for (int i = 0; i < 64; ++i) {
+        const bool same = __builtin_amdgcn_readlane(r.adapter, i) == r.adapter;
+        at += same && i < lane ? __builtin_amdgcn_readlane(r.tokens, i) : 0;
+        last = last && !(same && i > lane);
+      }
+      // counts end at n, which offsets that do not rise could pass
+      if (r.adapter >= 0) {
+        l.place[b + lane] = min(at, n);
+        if (last) l.count[r.adapter] = min(at + r.tokens, n);
+      }
+      __threadfence_block();   // the next 64 read these counts, other lanes' among them
+    }
+    // a list's cost: its tokens (none where its rank is zero) times the cost of a
+    // step at its rank
+    auto listed = [&](int a) { return a < nad && rank[a] > 0 ? l.count[a] : 0; };
     float cost = 0.0f;
     int busy = 0;
     for (int a = lane; a < nad; a += 64) {
-      cost += l.count[a] * step_cost(rank[a], rmax);
-      busy += l.count[a] > 0;
+      const int mine = listed(a);
+      cost += mine * step_cost(rank[a], rmax);
+      busy += mine > 0;
     }
     cost = wave_sum(cost);
     busy = __shfl(lane_prefix(busy), 63, 64);
@@ -172,8 +202,8 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
     int tokens = 0, chunks = 0, steps = 0;   // tokens: those that are not padding
     for (int b = 0; b < nad; b += 64) {
       const int a = b + lane;
-      // capped at n, which offsets that do not rise could pass
-      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(a < nad ? l.count[a] : 0));
+      // capped at n together too
+      const int64_t past = tokens + static_cast<int64_t>(lane_prefix(listed(a)));
       const int to = static_cast<int>(min(past, static_cast<int64_t>(n)));
       const int before = __shfl_up(to, 1, 64);
       const int mine = to - (lane == 0 ? tokens : before);
@@ -196,27 +226,21 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
     }
   }
   __syncthreads();
-  for (int a = wave; a < nad; a += WAVES) {
-    const int room = l.count[a];
-    if (room == 0) continue;
-    int at = 0;
-    for (int b = 0; b < nseg; b += 64) {
-      const int m = length(b + lane, a), p = lane_prefix(m);
-      if (m > 0) l.place[b + lane] = min(at + p - m, room);
-      at = min(at + __shfl(p, 63, 64), room);
+  for (int b = 64 * wave; b < nseg; b += 64 * WAVES) {
+    const Request r = request(b + lane);
+    int to = 0, tokens = 0;
+    if (r.adapter >= 0) {
+      const int count = l.count[r.adapter], start = l.start[r.adapter], place = l.place[b + lane];
+      to = start + place;
+      tokens = max(min(r.tokens, count - place), 0);
+      // the list's last token fills up its last step
+      if (tokens > 0 && place + tokens == count)
+        for (int q = count; q % 32 != 0; ++q) l.tokens[start + q] = r.first + tokens - 1;
     }
-  }
-  __syncthreads();
-  for (int s = wave; s < nseg; s += WAVES) {
-    const int a = ids[s];
-    if (a < 0 || a >= nad || l.count[a] == 0) continue;
-    const int first = request_start(off, s, nseg, n), m = request_start(off, s + 1, nseg, n) - first;
-    if (m <= 0) continue;
-    const int start = l.start[a], room = l.count[a], at = l.place[s];
-    for (int i = lane; i < m && at + i < room; i += 64) {
-      l.tokens[start + at + i] = first + i;
-      if (at + i == room - 1)
-        for (int q = room; q < (room + 31) / 32 * 32; ++q) l.tokens[start + q] = first + i;
+    for (uint64_t left = __ballot(tokens > 0); left != 0; left &= left - 1) {
+      const int i = __builtin_ctzll(left), first = __builtin_amdgcn_readlane(r.first, i);
+      const int to_i = __builtin_amdgcn_readlane(to, i), tokens_i = __builtin_amdgcn_readlane(tokens, i);
+      for (int q = lane; q < tokens_i; q += 64) l.tokens[to_i + q] = first + q;
     }
   }
 }

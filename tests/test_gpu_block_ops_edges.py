@@ -13,7 +13,7 @@ import aware_block_transforms_amd as W
 from aware_block_transforms_amd.layer import AdapterSet, W4A4Layer, request_table
 from oracle import block_ops as bo
 from gpu_util import DEV
-from test_gpu_block_ops import _norm_inputs, dev, f64, new
+from test_gpu_block_ops import Case, _norm_inputs, dev, f64, near, new
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +150,41 @@ def test_one_layer_with_adapters_on_two_streams_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, want[1]) and torch.equal(large, want[0]), turn
         assert all((c == turn).all() for c in canaries), turn
+
+
+# ----------------------------------------------------------------------------- adapters: many of them
+
+
+@pytest.mark.parametrize("n,nseg,nad,kind", [(3000, 200, 150, "ragged"), (300, 300, 70, "single"), (700, 65, 64, "ragged"),
+                                             (2500, 2500, 300, "single"), (257, 129, 65, "ragged")])
+def test_adapter_backward_of_many_adapters_and_requests(n, nseg, nad, kind):
+    # more than 64 adapters and requests; adapters without tokens, of rank 0, with many requests and with one
+    c = Case(301, n, 64, 72, nseg, nad, 16, kind=kind)
+    dY = dev(c.r.standard_normal((n, 72)), "bf16")
+    _, V = c.forward()
+    dX, dA, dB = new(n, 64), new(nad, 16, 64), new(nad, 16, 72)
+    ws = torch.full((W.wush_adapter_backward_ws_bytes(n, 64, 72, nseg, nad, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    W.wush_adapter_backward(dY, c.X, *c.dev, V, None, dX, dA, dB, ws=ws)
+    torch.cuda.synchronize()
+    ref, mag = bo.adapter_backward(f64(dY), f64(c.X), *c.plain(), f64(V), None)
+    near(dX, ref[0], mag[0], 72 + 16, "dX")
+    near(dA, ref[1], mag[1], 72 + n, "dA")
+    near(dB, ref[2], mag[2], n, "dBt")
+
+
+def test_time_of_many_adapters_and_requests():
+    # 4096 requests of a token over 1024 adapters: 64 turns of 64 requests, some microseconds each, and small products.
+    # Work that grew with requests times adapters took above 3 ms for a quarter of these adapters.
+    n, nad = 4096, 1024
+    c = Case(302, n, 64, 64, n, nad, 16, kind="single")
+    dY, V, dA, dB = dev(c.r.standard_normal((n, 64)), "bf16"), new(n, 16).zero_(), new(nad, 16, 64), new(nad, 16, 64)
+    ws = torch.empty(W.wush_adapter_backward_ws_bytes(n, 64, 64, n, nad, 16), dtype=torch.uint8, device=DEV)
+    best = np.inf
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        W.wush_adapter_backward(dY, c.X, *c.dev, V, None, None, dA, dB, ws=ws)
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    assert best < 2.0, best
