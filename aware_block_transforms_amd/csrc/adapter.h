@@ -105,6 +105,7 @@ __device__ __forceinline__ Tile find_tile(int number, int n, int nseg, const int
 // count [nad]: an adapter's tokens (0 where its rank is)
 // start [nad + 1]: where its list begins, a multiple of 32
 // chunk [nad + 1]: the number of its first chunk
+// part [nad]: the number of its first partial sum, where it has several chunks
 // span [nad]: tokens of its chunks, whole steps
 // place [nseg]: where a request's tokens begin
 struct Lists {
@@ -112,6 +113,7 @@ struct Lists {
   int* count;
   int* start;
   int* chunk;
+  int* part;
   int* span;
   int* place;
 };
@@ -199,7 +201,7 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
     busy = __shfl(lane_prefix(busy), 63, 64);
     // every list ends inside a chunk, half of one wasted on average
     const float share = cost / max(1, chunks_wanted - busy / 2);
-    int tokens = 0, chunks = 0, steps = 0;   // tokens: those that are not padding
+    int tokens = 0, chunks = 0, several = 0, steps = 0;   // tokens: those that are not padding
     for (int b = 0; b < nad; b += 64) {
       const int a = b + lane;
       // capped at n together too
@@ -209,16 +211,19 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
       const int mine = to - (lane == 0 ? tokens : before);
       const int span = a < nad ? 32 * max(kMinSteps, static_cast<int>(ceilf(share / (32.0f * step_cost(rank[a], rmax))))) : 32;
       const int parts = (mine + span - 1) / span, c = lane_prefix(parts);
+      const int kept = parts > 1 ? parts : 0, k = lane_prefix(kept);
       const int turns = (mine + 31) / 32, t = lane_prefix(turns);
       if (a < nad) {
         l.count[a] = mine;
         l.span[a] = span;
         l.start[a] = 32 * (steps + t - turns);
         l.chunk[a] = chunks + c - parts;
+        l.part[a] = several + k - kept;
       }
       tokens = __shfl(to, 63, 64);
       steps += __shfl(t, 63, 64);
       chunks += __shfl(c, 63, 64);
+      several += __shfl(k, 63, 64);
     }
     if (lane == 0) {
       l.start[nad] = 32 * steps;

@@ -132,7 +132,7 @@ struct Side {
   const uint8_t* scales;
   const float* s;   // [n][R]
   float* out;       // [nad][R][d]
-  float* part;      // [chunks][R][d]
+  float* part;      // [parts][R][d]
   int64_t ld;
   int d;
 };
@@ -296,7 +296,8 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 1 : 2) void adapter_grad_kern
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool left = blockIdx.x < wgs_a;
   const int64_t size = static_cast<int64_t>(R) * (left ? a.d : b.d);
-  float* out = chunks == 1 ? (left ? a.out : b.out) + ad * size : (left ? a.part : b.part) + number * size;
+  float* out = chunks == 1 ? (left ? a.out : b.out) + ad * size
+                           : (left ? a.part : b.part) + (l.part[ad] + number - before) * size;
   const int c0 = (left ? blockIdx.x : blockIdx.x - wgs_a) * kCols + 128 * wave;
   const int end = l.start[ad] + l.count[ad];
   // rows that do not count are left out of the chunks' parts
@@ -312,8 +313,8 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 1 : 2) void adapter_grad_kern
 __global__ __launch_bounds__(256) void adapter_join_kernel(Side a, Side b, int R, int nad,
                                                            const int* __restrict__ rank, Lists l) {
   const int ad = blockIdx.y;
-  const int first = l.chunk[ad], last = l.chunk[ad + 1];
-  if (last - first == 1) return;
+  const int chunks = l.chunk[ad + 1] - l.chunk[ad], first = l.part[ad], last = first + chunks;
+  if (chunks == 1) return;
   const bool left = blockIdx.z == 0;
   const float* part = left ? a.part : b.part;
   float* out = left ? a.out : b.out;
@@ -346,12 +347,19 @@ int chunks_wanted(int n, int d_in, int d_out, int rmax) {
 int64_t chunk_numbers(int n, int d_in, int d_out, int nad, int rmax) {
   return static_cast<int64_t>(chunks_wanted(n, d_in, d_out, rmax)) + nad;
 }
+// Partial sums there may be: chunks of adapters that have several.  Such an
+// adapter has less than twice as many as its tokens fill, and all together fill
+// no more than the chunks wanted.
+int64_t part_numbers(int n, int d_in, int d_out, int nad, int rmax) {
+  const int64_t all = chunk_numbers(n, d_in, d_out, nad, rmax), most = 2 * static_cast<int64_t>(chunks_wanted(n, d_in, d_out, rmax));
+  return all < most ? all : most;
+}
 int64_t step_numbers(int n, int nad) { return static_cast<int64_t>(n / 32) + nad; }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 size_t list_bytes(int n, int nseg, int nad) {
-  return round256(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4) + 4 * round256((static_cast<size_t>(nad) + 1) * 4) +
+  return round256(static_cast<size_t>(step_numbers(n, nad)) * 32 * 4) + 5 * round256((static_cast<size_t>(nad) + 1) * 4) +
          round256(static_cast<size_t>(nseg) * 4);
 }
 
@@ -372,7 +380,7 @@ namespace wush {
 
 size_t adapter_grads_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax) {
   return list_bytes(n, nseg, nad) +
-         static_cast<size_t>(chunk_numbers(n, d_in, d_out, nad, rmax)) * rmax * (static_cast<size_t>(d_in) + d_out) * sizeof(float);
+         static_cast<size_t>(part_numbers(n, d_in, d_out, nad, rmax)) * rmax * (static_cast<size_t>(d_in) + d_out) * sizeof(float);
 }
 
 ListJob adapter_lists(int n, int d_in, int d_out, int nseg, int nad, int rmax, void* ws) {
@@ -387,6 +395,7 @@ ListJob adapter_lists(int n, int d_in, int d_out, int nseg, int nad, int rmax, v
   job.l.count = take(static_cast<size_t>(nad) + 1);
   job.l.start = take(static_cast<size_t>(nad) + 1);
   job.l.chunk = take(static_cast<size_t>(nad) + 1);
+  job.l.part = take(static_cast<size_t>(nad) + 1);
   job.l.span = take(static_cast<size_t>(nad) + 1);
   job.l.place = take(nseg);
   return job;
@@ -405,7 +414,7 @@ wush_status adapter_grads(const char* who, wush_dtype gdt, int xkind, int n, int
   const Lists& l = job.l;
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + list_bytes(n, nseg, nad));
   const Side a{X, x_scales, dV, dA, part, ldx, d_in};
-  const Side b{dY, nullptr, V, dBt, part + numbers * rmax * d_in, ldg, d_out};
+  const Side b{dY, nullptr, V, dBt, part + part_numbers(n, d_in, d_out, nad, rmax) * rmax * d_in, ldg, d_out};
   // with tokens, the low kernel has made the lists
   if (n == 0)
     hipLaunchKernelGGL(adapter_list_kernel, dim3(1), dim3(256), 0, s, nseg, seg_off, seg_adapter, nad, rank, rmax, l);

@@ -22,3 +22,10 @@ def test_act8_refuses_rows_whose_columns_pass_31_bits(d):
     assert L.wush_act8_swiglu(1, 1, 1, d, P, P, d, P, P, P, P, P, None) == shape
     assert L.wush_act8_swiglu_bwd(1, 1, 1, d, P, P, P, P, P, P, P, d, None) == shape
     assert L.wush_act8_pack(1, 0, 2 ** 31 - 512, None, None, None, None) == W.WUSH_OK
+
+
+def test_adapter_workspace_grows_with_adapters_by_their_lists_alone():
+    # sums in parts are kept for adapters of several chunks only, and those are bounded by the launch
+    need = [L.wush_adapter_backward_ws_bytes(16384, 5120, 17408, 12, nad, 64) for nad in (100, 1000)]
+    assert 0 < need[1] - need[0] < 1 << 20, need
+    assert need[1] < 1 << 28

@@ -188,3 +188,22 @@ def test_time_of_many_adapters_and_requests():
         b.synchronize()
         best = min(best, a.elapsed_time(b))
     assert best < 2.0, best
+
+
+def test_adapter_backward_of_few_among_many_adapters():
+    # lists of several chunks between adapters without tokens: their partial sums lie side by side
+    n, nad, d_in, d_out = 6000, 100, 64, 72
+    c = Case(303, n, d_in, d_out, 7, nad, 16, ranks=[16] * nad)
+    c.off, c.ids = [0, 1800, 1900, 4300, 4301, 4600, 5999, 6000], [99, 0, 5, 6, -1, 70, 64]
+    c.dev = tuple(torch.tensor(a, dtype=torch.int32, device=DEV) for a in (c.off, c.ids)) + c.dev[2:]
+    dY = dev(c.r.standard_normal((n, d_out)), "bf16")
+    _, V = c.forward()
+    dA, dB = new(nad, 16, d_in), new(nad, 16, d_out)
+    need = W.wush_adapter_backward_ws_bytes(n, d_in, d_out, 7, nad, 16)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    W.wush_adapter_backward(dY, c.X, *c.dev, V, None, None, dA, dB, ws=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xFF).all()
+    ref, mag = bo.adapter_backward(f64(dY), f64(c.X), *c.plain(), f64(V), None)
+    near(dA, ref[1], mag[1], d_out + n, "dA")
+    near(dB, ref[2], mag[2], n, "dBt")
