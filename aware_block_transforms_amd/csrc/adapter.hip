@@ -53,8 +53,10 @@ constexpr int kWaves = 4;
 // lanes a row) and takes the operands out of its own part of LDS, where the
 // 16-byte chunks of row r are kept in the order c ^ (r mod the row's chunks), so
 // that the eight or sixteen rows of a read fall into different banks.  The next
-// piece is on its way, in registers, during the products of the one in LDS; no
-// barrier is needed.  Rows past the tile's tokens or the rank, and columns past
+// piece is on its way, in registers, during the products of the one in LDS.  The
+// lanes of a wave read what others of its lanes wrote: its LDS instructions take
+// effect in order, so no barrier is needed, only an order that the compiler keeps
+// (lds_order).  Rows past the tile's tokens or the rank, and columns past
 // d, lie outside the buffer resources and come as zeros.
 //
 // 16384 x 5120 in bf16 at rank 64: 42 us, 4.0 TB/s of X (55 us with operands
@@ -107,6 +109,12 @@ struct Piece {
   }
 };
 
+// Between a wave's writes to its part of LDS and its other lanes' reads of it,
+// both ways.  No instruction comes of it.
+__device__ __forceinline__ void lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
+
 // The operand of row tile i and k half h, lane 16 g + j: columns 8 (4 h + g) ..
 // of row 16 i + j.
 __device__ __forceinline__ void low_operand(const u32x4* lds, int i, int h, u32x4 (&t)[1], bf16_t) {
@@ -151,11 +159,13 @@ __device__ __forceinline__ void low_pieces(Piece<X, TT>& x, Piece<bf16_t, RT>& f
     for (int i = 0; i < whole; ++i) {
       x.template put<TT>(xl);
       f.template put<NT>(fl);
+      lds_order();
       // past the last piece it is loaded again: a branch would cost a wait
       const int next = k + min(i + 1, whole - 1) * step;
       x.template load<TT>(next);
       f.template load<NT>(next);
       multiply();
+      lds_order();
     }
   }
   k += whole * step;
@@ -164,8 +174,10 @@ __device__ __forceinline__ void low_pieces(Piece<X, TT>& x, Piece<bf16_t, RT>& f
     f.template load_tail<NT>(k);
     x.template put<TT>(xl);
     f.template put<NT>(fl);
+    lds_order();
     multiply();
   }
+  lds_order();
 }
 
 template <class X, int RT, int TT>

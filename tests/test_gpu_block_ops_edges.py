@@ -207,3 +207,14 @@ def test_adapter_backward_of_few_among_many_adapters():
     ref, mag = bo.adapter_backward(f64(dY), f64(c.X), *c.plain(), f64(V), None)
     near(dA, ref[1], mag[1], d_out + n, "dA")
     near(dB, ref[2], mag[2], n, "dBt")
+
+
+@pytest.mark.parametrize("xdt", ["bf16", "f32"])
+@pytest.mark.parametrize("rmax", [16, 32, 64, 128])
+@pytest.mark.parametrize("n,nseg", [(100, 4), (25, 1), (320, 9), (50, 3), (600, 5)])
+def test_adapter_forward_of_every_token_tile(n, nseg, rmax, xdt):
+    # requests of some 16 to 32 tokens, and longer ones; every number of row tiles of the factor, whole and partly used,
+    # and pieces of k that end inside one, at the last column and past several
+    for d_in in (64, 96, 1032):
+        c = Case(304, n, d_in, 40, nseg, 4, rmax, xdt, ranks=[rmax, rmax // 2 + 1, rmax // 4 + 1, rmax - 1])
+        c.check(*c.forward(), c.Y0)
