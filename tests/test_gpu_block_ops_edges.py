@@ -5,6 +5,9 @@ Bounds are those of test_gpu_block_ops: (K + 32) 2^-24 times the result computed
 for bf16 results.
 """
 
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -13,7 +16,9 @@ import aware_block_transforms_amd as W
 from aware_block_transforms_amd.layer import AdapterSet, W4A4Layer, request_table
 from oracle import block_ops as bo
 from gpu_util import DEV
-from test_gpu_block_ops import Case, _norm_inputs, dev, f64, near, new
+from test_gpu_block_ops import DT, TYPES, Case, _norm_check, _norm_grads, _norm_inputs, dev, f64, near, new
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +223,150 @@ def test_adapter_forward_of_every_token_tile(n, nseg, rmax, xdt):
     for d_in in (64, 96, 1032):
         c = Case(304, n, d_in, 40, nseg, 4, rmax, xdt, ranks=[rmax, rmax // 2 + 1, rmax // 4 + 1, rmax - 1])
         c.check(*c.forward(), c.Y0)
+
+
+# ----------------------------------------------------------------------------- block norm: wide rows, many rows
+
+
+LEFT_OUT = ["nothing", "dRout", "dR", "w_post", "w_pre", "Y"]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("n,d", [(530, 8200), (300, 16392)])
+def test_wide_norm_gradients_of_many_rows(n, d, types):
+    # a workgroup walks over several rows; every gate, and every tensor left out in turn
+    for i, gate in enumerate(["none", "channel", "token", "element"]):
+        r, Y, wp, g, R, w = _norm_inputs(102 + i, n, d, types, gate)
+        _norm_grads(r, Y, wp, g, R, w, types, 0.75, 1.25, d)
+    left = LEFT_OUT[1:] if types == TYPES[3] else LEFT_OUT[1 + TYPES.index(types) % 5:][:1]
+    for out in left:
+        r, Y, wp, g, R, w = _norm_inputs(110, n, d, types, "token")
+        _norm_grads(r, None if out == "Y" else Y, None if out in ("Y", "w_post") else wp, None if out == "Y" else g, R,
+                    None if out == "w_pre" else w, types, 0.75, 1.25, d, dr=out != "dRout", want_dR=out != "dR")
+
+
+@pytest.mark.parametrize("d", [12296, 16384, 20488, 24576])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "element"])
+def test_widest_norm_gradients(gate, d):
+    types = ("f32", "bf16", "bf16")
+    r, Y, wp, g, R, w = _norm_inputs(120, 270, d, types, gate)
+    _norm_grads(r, Y, wp, g, R, w, types, 1.0, 0.5, d)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("n,d", [(600, 520), (3, 12296), (3, 17408)])
+def test_norm_with_several_pieces_a_thread(n, d, types):
+    for gate in ("none", "channel", "token", "element"):
+        _, Y, wp, g, R, w = _norm_inputs(130, n, d, types, gate)
+        Rout, U, k1, k2 = new(n, d, dt=DT[types[1]]), new(n, d, dt=DT[types[2]]), new(n), new(n)
+        W.wush_block_norm(Y, wp, g, R, w, Rout, U, k1, k2, branch_scale=0.7, res_scale=0.9)
+        torch.cuda.synchronize()
+        _norm_check(Y, wp, g, R, w, np.float32(0.7), np.float32(0.9), np.float32(1e-6), Rout, U, k1, k2, d)
+
+
+# ----------------------------------------------------------------------------- outputs beyond the last-level cache
+# Outputs above 256 MB are written past the caches.  The same rows in two calls below that must give the same bits, and
+# the tests of small sizes hold those to the 64-bit form.
+
+
+def _rand(g, n, d, dt="f32"):
+    return torch.randn((n, d), generator=g, device=DEV).to(DT[dt])
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.mark.parametrize("types,n,d", [(("f32", "f32", "f32"), 2100, 16384), (("bf16", "f32", "f32"), 2100, 16392),
+                                       (("f32", "bf16", "bf16"), 4200, 16384), (("bf16", "bf16", "bf16"), 4200, 16392),
+                                       (("bf16", "f32", "bf16"), 2800, 16384), (("f32", "f32", "bf16"), 2800, 16392)])
+def test_norm_outputs_beyond_the_cache(types, n, d):
+    g, h = _gen(401), n // 2
+    Y, R, w = _rand(g, n, d, types[0]), _rand(g, n, d, types[1]), 1 + 0.1 * torch.randn(d, generator=g, device=DEV)
+    outs = [[torch.full((n, d), 7.0, dtype=DT[t], device=DEV) for t in types[1:]] for _ in range(2)]
+    assert n * d * sum(t[0].element_size() for t in zip(outs[0])) > 256 << 20
+    W.wush_block_norm(Y, w, None, R, w, *outs[0])
+    for a in (slice(0, h), slice(h, n)):
+        W.wush_block_norm(Y[a], w, None, R[a], w, outs[1][0][a], outs[1][1][a])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("hdt", ["f32", "bf16"])
+@pytest.mark.parametrize("xdt", ["f32", "bf16"])
+def test_gated_activation_outputs_beyond_the_cache(xdt, hdt):
+    g, d = _gen(402), 17408
+    n = 4200 if xdt == hdt == "f32" else 8200
+    x, dH = _rand(g, n, 2 * d, xdt), _rand(g, n, d, hdt)
+
+    def both(rows):
+        m = dH[rows].shape[0]
+        H = torch.full((m, d), 7.0, dtype=DT[hdt], device=DEV)
+        c = [torch.full((m, d // k), 99, dtype=t, device=DEV) for _ in range(2) for k, t in ((1, torch.int8), (32, torch.uint8))]
+        W.wush_act8_swiglu(x[rows, :d], x[rows, d:], H, *c)
+        H2 = torch.full_like(H, 7.0)
+        W.wush_act8_swiglu(x[rows, :d], x[rows, d:], H2)
+        dx = torch.full((m, 2 * d), 7.0, dtype=DT[xdt], device=DEV)
+        W.wush_act8_swiglu_bwd(dH[rows], *c, dx[:, :d], dx[:, d:])
+        back = torch.full((m, d), 7.0, dtype=DT[xdt], device=DEV)
+        W.wush_act8_unpack(c[0], c[1], back)
+        torch.cuda.synchronize()
+        return [H, H2, dx, back] + c
+    whole = both(slice(0, n))
+    assert whole[0].numel() * whole[0].element_size() > 256 << 20
+    for a in range(0, n, n // 4):
+        rows = slice(a, min(n, a + n // 4))
+        assert all(torch.equal(w[rows], p) for w, p in zip(whole, both(rows))), a
+
+
+@pytest.mark.parametrize("rmax", [16, 32, 64, 128])
+@pytest.mark.parametrize("ydt", ["f32", "bf16"])
+def test_adapter_outputs_beyond_the_cache(ydt, rmax):
+    # every request's rows at its first, middle and last tokens against the 64-bit form; with and without a base
+    n, d_in, d_out = (4100, 264, 17408) if ydt == "f32" else (8200, 264, 17408)
+    c = Case(403, n, d_in, d_out, 9, 4, rmax, ydt=ydt, ranks=[rmax, rmax // 2 + 1, 7, 0])
+    assert c.Y0.numel() * c.Y0.element_size() > 256 << 20
+    rows = sorted({t for a, b in zip(c.off, c.off[1:]) if a < b for t in (a, min(a + 63, b - 1), (a + b) // 2, b - 1)})
+    # a request of one token for each of these rows
+    ids = [c.ids[next(s for s in range(len(c.ids)) if c.off[s] <= t < c.off[s + 1])] for t in rows]
+    for base in (c.Y0, None):
+        Y, V = c.forward(Y0=base)
+        plain = (list(range(len(rows) + 1)), ids) + c.plain()[2:]
+        ref, mag = bo.adapter_forward(f64(c.X[rows]), *plain, None if base is None else f64(base[rows]), d_out)
+        near(Y[rows], ref[0], mag[0], d_in + rmax, "Y")
+        near(V[rows], ref[1], mag[1], d_in, "V")
+        assert torch.isfinite(Y).all()
+
+
+# ----------------------------------------------------------------------------- the fine-tuning example
+
+
+def test_example_gradients_of_both_adapter_sets_against_the_formulas():
+    # the example's backward pass against the 64-bit forms, from what its forward pass kept.  dY, dH and dGU are rounded
+    # to bf16 between the steps, and dY W before it is added: four roundings of at most 2^-9 of a value each, which the
+    # sums carry on; their norm is within 4 * 2^-9 of the result's, twice that with the terms' cancellation
+    from finetune_mlp import MlpBlock
+    g, n, d, h = _gen(501), 200, 256, 512
+    block = MlpBlock(d, h, nad=2)
+    R, c = _rand(g, n, d, "bf16"), _rand(g, n, d, "bf16")
+    lengths, ids = [70, 30, 100], [0, -1, 1]
+    req, off = request_table(lengths, ids), [0, 70, 100, 200]
+    for ad in (block.ad_gu, block.ad_dn):
+        ad.Bt.copy_(torch.randn(ad.Bt.shape, generator=g, device=DEV) * 0.1)
+    _, kept = block.forward(R, req, train=True)
+    grads = block.backward(c, req, kept)
+    torch.cuda.synchronize()
+    (u8, us), V1, (gc, gs, uc, uss), (h8, hs), V2, Y, Rout, k1, k2 = kept
+    val = lambda q, s: bo.act8_values(q.cpu().numpy(), s.cpu().numpy())  # noqa: E731
+
+    def adapters(ad, dY, X, V, dX0):
+        return bo.adapter_backward(dY, X, off, ids, f64(ad.A), f64(ad.Bt), [16, 16], [1.0, 1.0], f64(V), dX0)[0]
+    dY = bo.block_norm_bwd(f64(c), None, f64(Y), f64(block.w_post), f64(block.scale), f64(Rout), f64(block.w_out), f64(k1),
+                           f64(k2), 1.0, 1.0)["dY"]
+    dH, dA2, dB2 = adapters(block.ad_dn, dY, val(h8, hs), V2, dY @ f64(block.Wdn))
+    dG, dU = bo.swiglu_bwd(dH, val(gc, gs), val(uc, uss))
+    _, dA1, dB1 = adapters(block.ad_gu, np.concatenate([dG, dU], axis=1), val(u8, us), V1, None)
+    for got, ref in zip((t for pair in grads for t in pair), (dA1, dB1, dA2, dB2)):
+        assert np.linalg.norm(f64(got) - ref) <= 8 * 2.0 ** -9 * np.linalg.norm(ref)
