@@ -123,8 +123,10 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream
-    # the current stream's handle without the Stream object around it (0.4 instead of 3 us)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the current stream's handle without the Stream object around it (0.4 instead of 3 us), where this torch gives it:
+    # the function is not part of its documented interface
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
 
 
 def _fmt(fmt):
