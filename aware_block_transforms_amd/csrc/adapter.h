@@ -19,7 +19,8 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 // that a product with a bf16 operand rounds nowhere but in the fp32 sums.  The
 // other way, one bf16 term, costs two thirds of the matrix work less and loses
 // two bytes of every intermediate; these kernels wait for memory instead.  An
-// infinity splits into an infinity and NaN: results it reaches are NaN.
+// infinity splits into an infinity and NaN, and one in the other operand meets
+// terms that are zero: results that either reaches are NaN.
 __device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
   a = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
   const float r1 = v - __builtin_bit_cast(float, a);

@@ -512,7 +512,8 @@ wush_status wush_act8_swiglu_bwd(wush_dtype hdt, wush_dtype xdt, int n, int d, c
  *   ws    device scratch of wush_adapter_ws_bytes(n, d_in, nseg, rmax) bytes, or
  *         NULL (taken from the default memory pool for the call).
  * V is held and used as fp32 (split into exact bf16 terms for the matrix
- * cores), and sums are fp32.  An infinity in V makes its results NaN.
+ * cores), and sums are fp32.  An infinity in V, or in an fp32 X, makes the
+ * results it reaches NaN.
  * Errors: WUSH_E_ARG, WUSH_E_SHAPE (n above 2^24, nseg outside 1..2^20, nad below
  * 1, rmax, a row length or stride that is no multiple of 8, a row stride below the
  * row's length or above 2^22 values), WUSH_E_HIP. */
@@ -537,10 +538,11 @@ wush_status wush_adapter_forward(wush_dtype xdt, wush_dtype ydt, int n, int d_in
  *         dX0, or NULL if not wanted.
  *   dA, dBt  device out, fp32, shaped like A and Bt.
  *   ws    device scratch of wush_adapter_backward_ws_bytes(...) bytes, or NULL.
- * n = 0 clears dA and dBt.  An infinity in V, dV, or an fp32 X or dY makes the
- * results it reaches NaN.  Errors: as above; also WUSH_E_SHAPE for so many
- * adapters that the launch does not hold them (from some 65000), or act8 codes
- * whose d_in is no multiple of 32 or whose rows are not packed. */
+ * n = 0 clears dA and dBt.  An infinity in V, dV, X or dY, of either type, makes
+ * the results it reaches NaN.  Errors: as above, but the stride of X has no upper
+ * limit; also WUSH_E_SHAPE for so many adapters that the launch does not hold
+ * them (from some 65000), or act8 codes whose d_in is no multiple of 32 or whose
+ * rows are not packed. */
 size_t wush_adapter_backward_ws_bytes(int n, int d_in, int d_out, int nseg, int nad, int rmax);
 wush_status wush_adapter_backward(wush_dtype gdt, wush_dtype xdt, wush_dtype ydt, int n, int d_in,
                                   int d_out, const void* dY, int64_t ldg, const void* X,

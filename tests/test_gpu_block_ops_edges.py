@@ -370,3 +370,36 @@ def test_example_gradients_of_both_adapter_sets_against_the_formulas():
     _, dA1, dB1 = adapters(block.ad_gu, np.concatenate([dG, dU], axis=1), val(u8, us), V1, None)
     for got, ref in zip((t for pair in grads for t in pair), (dA1, dB1, dA2, dB2)):
         assert np.linalg.norm(f64(got) - ref) <= 8 * 2.0 ** -9 * np.linalg.norm(ref)
+
+
+# ----------------------------------------------------------------------------- adapters: infinities
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_adapter_gradients_reached_by_an_infinity(dt):
+    # not finite where the infinity reaches, bit by bit the same elsewhere
+    c = Case(305, 90, 264, 136, 3, 3, 16, dt, ranks=[16, 9, 16])
+    c.off, c.ids = [0, 30, 60, 90], [0, 1, 2]
+    c.dev = tuple(torch.tensor(a, dtype=torch.int32, device=DEV) for a in (c.off, c.ids)) + c.dev[2:]
+    dY = dev(c.r.standard_normal((90, 136)), dt)
+    _, V = c.forward()
+
+    def grads(X, dY):
+        dX, dA, dB = new(90, 264), new(3, 16, 264), new(3, 16, 136)
+        W.wush_adapter_backward(dY, X, *c.dev, V, None, dX, dA, dB)
+        torch.cuda.synchronize()
+        return dX, dA, dB
+    want = grads(c.X, dY)
+    X = c.X.clone()
+    X[40, 11] = float("inf")                      # a token of adapter 1: column 11 of its dA
+    dX, dA, dB = grads(X, dY)
+    assert torch.equal(dX, want[0]) and torch.equal(dB, want[2])
+    assert not torch.isfinite(dA[1, :9, 11]).any()
+    dA[1, :9, 11] = want[1][1, :9, 11]
+    assert torch.equal(dA, want[1])
+    bad = dY.clone()
+    bad[70, 5] = float("-inf")                    # one of adapter 2: its row of dX, all of dA, column 5 of dBt
+    dX, dA, dB = grads(c.X, bad)
+    assert not torch.isfinite(dX[70]).any() and not torch.isfinite(dA[2]).any() and not torch.isfinite(dB[2, :, 5]).any()
+    dX[70], dA[2], dB[2, :, 5] = want[0][70], want[1][2], want[2][2, :, 5]
+    assert all(torch.equal(a, b) for a, b in zip((dX, dA, dB), want))
