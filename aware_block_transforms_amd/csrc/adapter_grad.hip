@@ -332,12 +332,15 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(Side a, Side b, int R
 }
 
 // Chunks wanted: so many that the workgroups fit the compute units once (two on
-// each; three at rank 16, one at rank 128), since a second round for the last
-// few would take as long as the first.  With the join, the two cases above take
-// 36 and 96 us; 45 and 162 with half as many, 49 and 107 with twice as many.
+// each, one at rank 128), since a second round for the last few would take as
+// long as the first.  The backward call without dX, two adapters, 4096 tokens of
+// 4096 + 12288 and 16384 of 5120 + 5120 bf16 columns: 54 and 100 us at rank 16
+// (with 256 more workgroups, which still fit, 56 and 105), 61 and 110 at rank 32,
+// 79 and 143 at rank 64, 130 and 254 at rank 128; at ranks 32 to 128 with half as
+// many 66 to 180 and 136 to 389, with twice as many 71 to 158 and 123 to 275.
 int chunks_wanted(int n, int d_in, int d_out, int rmax) {
   const int wgs = (d_in + kCols - 1) / kCols + (d_out + kCols - 1) / kCols;
-  const int slots = rmax == 16 ? 768 : rmax == 128 ? 256 : 512;
+  const int slots = rmax == 128 ? 256 : 512;
   const int least = n / (32 * kMinSteps) + 1;
   const int c = slots / wgs;
   return c < 1 ? 1 : c < least ? c : least;
