@@ -144,23 +144,26 @@ __device__ __forceinline__ float step_cost(int rank, int rmax) {
 // and with the adapters, not with their product: one wave goes over the requests,
 // 64 at a time, and counts the tokens of every adapter as it finds each request's
 // place among them; the lists' lengths then give the chunks, and all waves write
-// the tokens.  Few requests hide behind the low kernel.  Many do not: some 7 us
-// for each 64 requests (16384 tokens, 4096 + 4096 columns at rank 16, the whole
+// the tokens.  Up to 64 requests stay in the lanes of every wave, and the counts of
+// few adapters in `lds` (of `room` integers), since each turn through memory costs
+// most of a microsecond: so few hide behind the low kernel.  Many do not: some 7
+// us for each 64 requests (16384 tokens, 4096 + 4096 columns at rank 16, the whole
 // backward call: 158 us for 12 requests of 4 adapters, 173 for 128 of 32, 219 for
 // 512 of 128, 700 for 4096 of 256; with a wave that went over all requests for
 // each adapter 158, 204, 440 and 3097).
 template <int WAVES>
 __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, const int* ids, int nad, const int* rank,
-                                            int rmax, int chunks_wanted, const Lists& l) {
+                                            int rmax, int chunks_wanted, int* lds, int room, const Lists& l) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int a = threadIdx.x; a < nad; a += 64 * WAVES) l.count[a] = 0;
-  __syncthreads();
-  // a request's adapter (-1: none), first token and tokens
+  const bool few = nseg <= 64;
+  int* found = nad <= room ? lds : l.count;
+  // a request's adapter (-1: none), first token and tokens, and how many tokens of
+  // its adapter come before it
   struct Request {
-    int adapter, first, tokens;
+    int adapter, first, tokens, place;
   };
   auto request = [&](int s) {
-    Request r{-1, 0, 0};
+    Request r{-1, 0, 0, 0};
     if (s >= nseg) return r;
     const int a = ids[s];
     r.first = request_start(off, s, nseg, n);
@@ -168,38 +171,44 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
     if (a >= 0 && a < nad && r.tokens > 0) r.adapter = a;
     return r;
   };
-  if (wave == 0) {
-    Request next = request(lane);
+  Request next = request(lane);
+  for (int a = threadIdx.x; a < nad; a += 64 * WAVES) found[a] = 0;
+  __syncthreads();
+  Request r = next;
+  if (few || wave == 0) {
     for (int b = 0; b < nseg; b += 64) {
-      const Request r = next;
-      next = request(b + 64 + lane);
-      int at = b > 0 && r.adapter >= 0 ? l.count[r.adapter] : 0;
+      r = next;
+      if (!few) next = request(b + 64 + lane);
+      int at = b > 0 && r.adapter >= 0 ? found[r.adapter] : 0;
       bool last = true;   // of its adapter's requests among the 64
-#pragma unroll 8
-      for (int i = 0; i < 64; ++i) {
+      const int count = min(nseg - b, 64);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
         const bool same = __builtin_amdgcn_readlane(r.adapter, i) == r.adapter;
         at += same && i < lane ? __builtin_amdgcn_readlane(r.tokens, i) : 0;
         last = last && !(same && i > lane);
       }
       // counts end at n, which offsets that do not rise could pass
-      if (r.adapter >= 0) {
-        l.place[b + lane] = min(at, n);
-        if (last) l.count[r.adapter] = min(at + r.tokens, n);
+      r.place = min(at, n);
+      if (r.adapter >= 0 && wave == 0) {
+        if (!few) l.place[b + lane] = r.place;
+        if (last) found[r.adapter] = min(at + r.tokens, n);
       }
-      __threadfence_block();   // the next 64 read these counts, other lanes' among them
+      __threadfence_block();   // other lanes read these counts
     }
+  }
+  if (wave == 0) {
     // a list's cost: its tokens (none where its rank is zero) times the cost of a
     // step at its rank
-    auto listed = [&](int a) { return a < nad && rank[a] > 0 ? l.count[a] : 0; };
+    auto listed = [&](int a) { return a < nad && rank[a] > 0 ? found[a] : 0; };
     float cost = 0.0f;
     int busy = 0;
-    for (int a = lane; a < nad; a += 64) {
-      const int mine = listed(a);
-      cost += mine * step_cost(rank[a], rmax);
-      busy += mine > 0;
+    for (int b = 0; b < nad; b += 64) {
+      const int mine = listed(b + lane);
+      if (mine > 0) cost += mine * step_cost(rank[b + lane], rmax);
+      busy += __popcll(__ballot(mine > 0));
     }
     cost = wave_sum(cost);
-    busy = __shfl(lane_prefix(busy), 63, 64);
     // every list ends inside a chunk, half of one wasted on average
     const float share = cost / max(1, chunks_wanted - busy / 2);
     int tokens = 0, chunks = 0, several = 0, steps = 0;   // tokens: those that are not padding
@@ -211,8 +220,10 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
       const int before = __shfl_up(to, 1, 64);
       const int mine = to - (lane == 0 ? tokens : before);
       const int span = a < nad ? 32 * max(kMinSteps, static_cast<int>(ceilf(share / (32.0f * step_cost(rank[a], rmax))))) : 32;
-      const int parts = (mine + span - 1) / span, c = lane_prefix(parts);
-      const int kept = parts > 1 ? parts : 0, k = lane_prefix(kept);
+      // chunks and those of adapters with several: at most 2^16 - 1 in all (the
+      // launch's limit), and fewer, in the halves of one sum
+      const int parts = (mine + span - 1) / span, kept = parts > 1 ? parts : 0;
+      const int both = lane_prefix(parts | kept << 16), c = both & 0xffff, k = both >> 16;
       const int turns = (mine + 31) / 32, t = lane_prefix(turns);
       if (a < nad) {
         l.count[a] = mine;
@@ -221,10 +232,10 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
         l.chunk[a] = chunks + c - parts;
         l.part[a] = several + k - kept;
       }
-      tokens = __shfl(to, 63, 64);
-      steps += __shfl(t, 63, 64);
-      chunks += __shfl(c, 63, 64);
-      several += __shfl(k, 63, 64);
+      tokens = __builtin_amdgcn_readlane(to, 63);
+      steps += __builtin_amdgcn_readlane(t, 63);
+      chunks += __builtin_amdgcn_readlane(c, 63);
+      several += __builtin_amdgcn_readlane(k, 63);
     }
     if (lane == 0) {
       l.start[nad] = 32 * steps;
@@ -232,21 +243,26 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
     }
   }
   __syncthreads();
-  for (int b = 64 * wave; b < nseg; b += 64 * WAVES) {
-    const Request r = request(b + lane);
+  // few requests: every wave a share of each one's tokens; many: of the requests
+  const int turn = few ? 64 * WAVES : 64;
+  for (int b = few ? 0 : 64 * wave; b < nseg; b += 64 * WAVES) {
+    if (!few) {
+      r = request(b + lane);
+      r.place = r.adapter >= 0 ? l.place[b + lane] : 0;
+    }
     int to = 0, tokens = 0;
     if (r.adapter >= 0) {
-      const int count = l.count[r.adapter], start = l.start[r.adapter], place = l.place[b + lane];
-      to = start + place;
-      tokens = max(min(r.tokens, count - place), 0);
+      const int count = l.count[r.adapter], start = l.start[r.adapter];
+      to = start + r.place;
+      tokens = max(min(r.tokens, count - r.place), 0);
       // the list's last token fills up its last step
-      if (tokens > 0 && place + tokens == count)
+      if (tokens > 0 && r.place + tokens == count && (wave == 0 || !few))
         for (int q = count; q % 32 != 0; ++q) l.tokens[start + q] = r.first + tokens - 1;
     }
     for (uint64_t left = __ballot(tokens > 0); left != 0; left &= left - 1) {
       const int i = __builtin_ctzll(left), first = __builtin_amdgcn_readlane(r.first, i);
       const int to_i = __builtin_amdgcn_readlane(to, i), tokens_i = __builtin_amdgcn_readlane(tokens, i);
-      for (int q = lane; q < tokens_i; q += 64) l.tokens[to_i + q] = first + q;
+      for (int q = few ? threadIdx.x : lane; q < tokens_i; q += turn) l.tokens[to_i + q] = first + q;
     }
   }
 }

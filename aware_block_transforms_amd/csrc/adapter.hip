@@ -193,7 +193,9 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_low_kernel(int n, int d, 
   constexpr int kPieces = (Piece<X, TT>::kBytes + Piece<bf16_t, RT>::kBytes) / 16, kSums = 16 * R / 4;
   __shared__ u32x4 lds[kWaves][kPieces > kSums ? kPieces : kSums];
   if (job.on && blockIdx.x == 0) {
-    if (blockIdx.y == 0) list_tokens<kWaves>(n, nseg, off, ids, nad, rank, R, job.chunks_wanted, job.l);
+    if (blockIdx.y == 0)
+      list_tokens<kWaves>(n, nseg, off, ids, nad, rank, R, job.chunks_wanted, reinterpret_cast<int*>(lds),
+                          sizeof(lds) / sizeof(int), job.l);
     return;
   }
   const Tile t = find_tile<T>(blockIdx.x - job.on, n, nseg, off, ids, nad);

@@ -44,7 +44,7 @@ constexpr int kCols = 128 * kWaves;
 // The lists of no tokens.
 __global__ __launch_bounds__(256) void adapter_list_kernel(int nseg, const int* off, const int* ids, int nad,
                                                            const int* rank, int rmax, Lists l) {
-  list_tokens<4>(0, nseg, off, ids, nad, rank, rmax, 1, l);
+  list_tokens<4>(0, nseg, off, ids, nad, rank, rmax, 1, nullptr, 0, l);
 }
 
 // Adapter of a step or chunk `number`: the last one whose first is not past it.
