@@ -243,10 +243,11 @@ __device__ __forceinline__ void grad_steps(const Side& side, int c, int first, i
   }
 }
 
-template <class X, int RT>
+// `where` gives the place of the results: it is looked up after the steps, which
+// have no registers to spare for it.
+template <class X, int RT, class F>
 __device__ __forceinline__ void grad_tile(const Side& side, int c0, int first, int last, int end, int rk,
-                                          int rows, const int* __restrict__ tokens, Shared<RT>* ops,
-                                          float* __restrict__ out) {
+                                          int rows, const int* __restrict__ tokens, Shared<RT>* ops, F where) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   // waves and lanes past the last column repeat it: they still share the work
   // on S, and store nothing
@@ -267,6 +268,7 @@ __device__ __forceinline__ void grad_tile(const Side& side, int c0, int first, i
   else
     grad_steps<X, 1, RT>(side, c, first, last, end, tokens, ops, acc);
   if (col >= side.d) return;
+  float* __restrict__ out = where();
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -295,17 +297,19 @@ __global__ __launch_bounds__(64 * kWaves, RT > 4 ? 1 : 2) void adapter_grad_kern
   const int rk = min(rank[ad], R);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool left = blockIdx.x < wgs_a;
-  const int64_t size = static_cast<int64_t>(R) * (left ? a.d : b.d);
-  float* out = chunks == 1 ? (left ? a.out : b.out) + ad * size
-                           : (left ? a.part : b.part) + (l.part[ad] + number - before) * size;
+  auto where = [&]() {
+    const int64_t size = static_cast<int64_t>(R) * (left ? a.d : b.d);
+    return chunks == 1 ? (left ? a.out : b.out) + ad * size
+                       : (left ? a.part : b.part) + (l.part[ad] + number - l.chunk[ad]) * size;
+  };
   const int c0 = (left ? blockIdx.x : blockIdx.x - wgs_a) * kCols + 128 * wave;
   const int end = l.start[ad] + l.count[ad];
   // rows that do not count are left out of the chunks' parts
   const int rows = chunks == 1 ? R : rk;
   if (left)
-    grad_tile<X, RT>(a, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, out);
+    grad_tile<X, RT>(a, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, where);
   else
-    grad_tile<G, RT>(b, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, out);
+    grad_tile<G, RT>(b, c0, first / 32, last / 32, end, rk, rows, l.tokens, ops, where);
 }
 
 // Sums the chunks of the adapters that have several, clears those of none and
