@@ -60,12 +60,29 @@ __device__ __forceinline__ int request_start(const int* __restrict__ off, int s,
   return s <= 0 ? 0 : s >= nseg ? n : min(max(off[s], 0), n);
 }
 
+// The last of `count` items whose first(item) is not past `number`, -1 if there is
+// none; first must rise.  A wave looks at 64 items that lie evenly apart at a
+// time, and a 64th is left: two turns for 4096.
+template <class F>
+__device__ __forceinline__ int last_not_past(int count, int number, F first) {
+  int s = 0, below = count;   // it lies in [s, below)
+  for (;;) {
+    const int step = (below - s + 63) / 64, q = s + (threadIdx.x & 63) * step;
+    const int c = __popcll(__ballot(q < below && first(q) <= number));
+    if (c == 0) return -1;
+    s = __builtin_amdgcn_readfirstlane(s + (c - 1) * step);
+    if (step == 1) return s;
+    below = min(s + step, below);
+  }
+}
+
 template <int T>
 __device__ __forceinline__ Tile find_tile(int number, int n, int nseg, const int* __restrict__ off,
                                           const int* __restrict__ ids, int nad) {
-  // every wave counts the requests whose first tile is not past `number`; the
-  // count's last request is the tile's.  Of up to 64 requests the lanes hold
-  // everything needed, one load after another is saved.
+  // the tile's request is the last one whose first tile is not past `number`.  Of
+  // up to 64 requests the lanes hold everything needed; one load after another is
+  // saved.  65536 requests of a token, 64 -> 64 at rank 16: 0.38 ms, 22 where every
+  // workgroup looked at all of them; 4096 requests 29 us and 112.
   const int lane = threadIdx.x & 63;
   Tile t{0, 0, -1};
   int s, first, last, a;
@@ -79,12 +96,7 @@ __device__ __forceinline__ Tile find_tile(int number, int n, int nseg, const int
     last = s + 1 < nseg ? __builtin_amdgcn_readlane(start, s + 1) : n;
     a = __builtin_amdgcn_readlane(id, s);
   } else {
-    int count = 0;
-    for (int b = 0; b < nseg; b += 64) {
-      const int q = b + lane;
-      count += __popcll(__ballot(q < nseg && request_start(off, q, nseg, n) / T + q <= number));
-    }
-    s = __builtin_amdgcn_readfirstlane(count - 1);
+    s = last_not_past(nseg, number, [&](int q) { return request_start(off, q, nseg, n) / T + q; });
     if (s < 0) return t;
     first = request_start(off, s, nseg, n);
     last = request_start(off, s + 1, nseg, n);
@@ -146,11 +158,12 @@ __device__ __forceinline__ float step_cost(int rank, int rmax) {
 // place among them; the lists' lengths then give the chunks, and all waves write
 // the tokens.  Up to 64 requests stay in the lanes of every wave, and the counts of
 // few adapters in `lds` (of `room` integers), since each turn through memory costs
-// most of a microsecond: so few hide behind the low kernel.  Many do not: some 7
+// most of a microsecond: so few hide behind the low kernel.  Many do not: some 6
 // us for each 64 requests (16384 tokens, 4096 + 4096 columns at rank 16, the whole
-// backward call: 158 us for 12 requests of 4 adapters, 173 for 128 of 32, 219 for
-// 512 of 128, 700 for 4096 of 256; with a wave that went over all requests for
-// each adapter 158, 204, 440 and 3097).
+// backward call: 153 us for 12 requests of 4 adapters, 169 for 128 of 32, 206 for
+// 512 of 128, 556 for 4096 of 256; with a wave that went over all requests for
+// each adapter, and workgroups that looked at all requests, 158, 204, 440 and
+// 3097).
 template <int WAVES>
 __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, const int* ids, int nad, const int* rank,
                                             int rmax, int chunks_wanted, int* lds, int room, const Lists& l) {
@@ -181,12 +194,13 @@ __device__ __forceinline__ void list_tokens(int n, int nseg, const int* off, con
       if (!few) next = request(b + 64 + lane);
       int at = b > 0 && r.adapter >= 0 ? found[r.adapter] : 0;
       bool last = true;   // of its adapter's requests among the 64
-      const int count = min(nseg - b, 64);
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const bool same = __builtin_amdgcn_readlane(r.adapter, i) == r.adapter;
-        at += same && i < lane ? __builtin_amdgcn_readlane(r.tokens, i) : 0;
-        last = last && !(same && i > lane);
+      for (int first = 0; first < min(nseg - b, 64); first += 8) {
+#pragma unroll
+        for (int i = first; i < first + 8; ++i) {
+          const bool same = __builtin_amdgcn_readlane(r.adapter, i) == r.adapter;
+          at += same && i < lane ? __builtin_amdgcn_readlane(r.tokens, i) : 0;
+          last = last && !(same && i > lane);
+        }
       }
       // counts end at n, which offsets that do not rise could pass
       r.place = min(at, n);

@@ -403,3 +403,47 @@ def test_adapter_gradients_reached_by_an_infinity(dt):
     assert not torch.isfinite(dX[70]).any() and not torch.isfinite(dA[2]).any() and not torch.isfinite(dB[2, :, 5]).any()
     dX[70], dA[2], dB[2, :, 5] = want[0][70], want[1][2], want[2][2, :, 5]
     assert all(torch.equal(a, b) for a, b in zip((dX, dA, dB), want))
+
+
+# ----------------------------------------------------------------------------- adapters: very many requests
+
+
+@pytest.mark.parametrize("nseg", [65, 4096, 4097, 9000])
+def test_adapter_of_very_many_requests(nseg):
+    # requests of no token, one and several, more than one and two counts of 64 find
+    r = np.random.default_rng(306)
+    lengths = r.choice([0, 0, 1, 1, 1, 2, 5, 17], nseg)
+    n, nad = int(lengths.sum()), 5
+    c = Case(306, n, 64, 40, 2, nad, 16, ranks=[16, 16, 9, 0, 16])
+    c.off, c.ids = [0] + [int(v) for v in np.cumsum(lengths)], [int(v) for v in r.integers(-1, nad, nseg)]
+    c.dev = tuple(torch.tensor(a, dtype=torch.int32, device=DEV) for a in (c.off, c.ids)) + c.dev[2:]
+    Y, V = c.forward()
+    c.check(Y, V, c.Y0)
+    dY = dev(c.r.standard_normal((n, 40)), "bf16")
+    dX, dA, dB = new(n, 64), new(nad, 16, 64), new(nad, 16, 40)
+    W.wush_adapter_backward(dY, c.X, *c.dev, V, None, dX, dA, dB)
+    torch.cuda.synchronize()
+    ref, mag = bo.adapter_backward(f64(dY), f64(c.X), *c.plain(), f64(V), None)
+    near(dX, ref[0], mag[0], 40 + 16, "dX")
+    near(dA, ref[1], mag[1], 40 + n, "dA")
+    near(dB, ref[2], mag[2], n, "dBt")
+
+
+def test_time_of_very_many_requests():
+    # 65536 requests of a token: work that grows with the requests, some 130000 short workgroups, takes about a
+    # millisecond; where each workgroup looked at all requests it took 22
+    n = 65536
+    A = torch.zeros((8, 16, 64), dtype=torch.bfloat16, device=DEV)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)  # noqa: E731
+    args = (i32(range(n + 1)), i32(np.arange(n) % 8), A, A, i32([16] * 8), torch.ones(8, device=DEV))
+    X, Y = torch.zeros((n, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((n, 64), device=DEV)
+    ws = torch.empty(W.wush_adapter_ws_bytes(n, 64, n, 16), dtype=torch.uint8, device=DEV)
+    best = np.inf
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        W.wush_adapter_forward(X, *args, Y, Y, ws=ws)
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    assert best < 5.0, best
