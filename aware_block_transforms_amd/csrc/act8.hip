@@ -231,8 +231,10 @@ __global__ __launch_bounds__(64 * kWaves) void act8_unpack_kernel(int64_t n, int
   }
 }
 
-// 1 / (1 + exp(-x)) on the transcendental unit: 1 to 2 ulp where it matters
-// (for x below -20 the relative error grows with |x|, on values below 1e-8).
+// 1 / (1 + exp(-x)) on the transcendental unit.  For positive x 1 to 2 ulp.  For
+// negative x the rounding of 1.44 x shows: some |x| ulp (4 at -5, 15 at -16), and
+// below -88 the result, at most 1e-38, becomes zero.  Splitting the product in two
+// would remove it; results that are kept as bf16 or 8-bit codes do not see it.
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
 }

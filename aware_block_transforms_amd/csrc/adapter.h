@@ -143,8 +143,12 @@ __device__ __forceinline__ int lane_prefix(int v) {   // inclusive
 
 // Steps of a chunk at least, so that its start and its part of the join stay
 // small beside it (it matters only to short calls), and the relative cost of a
-// step: what the rows take, and the products of each row tile (16384 tokens, four
-// adapters of rank 8 to 64, act8 X: 85 us, with all steps taken as equal 94).
+// step: what the rows take, and the products of each row tile.  Four adapters of
+// ranks between 8 and rmax, all steps taken as equal against these costs: the grad
+// kernel on 16384 tokens with act8 X at 64 94 and 85 us; the backward call without
+// dX on 16384 tokens, 5120 + 5120 bf16 columns, 110 and 109 us at rmax 32, 125 and
+// 120 at 64, 241 and 203 at 128, on 4096 tokens, 4096 + 12288, 59 and 58, 73 and 70,
+// 123 and 108.
 constexpr int kMinSteps = 4;
 __device__ __forceinline__ float step_cost(int rank, int rmax) {
   const int tiles = (min(max(rank, 1), rmax) + 15) / 16;

@@ -15,13 +15,16 @@
 // belongs to is free to choose: operand c of lane j is column 8 j + c.  A wave
 // owns 128 columns.  The four waves of a workgroup walk over the same tokens
 // and share the operands of S, which they split into three bf16 terms together,
-// one step ahead, through two LDS buffers.  The rows of X are loaded one step
-// ahead too, into the registers that the step's operands have just left.
+// one step ahead, through two LDS buffers.  The rows of a bf16 or act8 X are loaded
+// one step ahead too, into the registers that the step's operands have just left.
+// Those of an fp32 X (or dY), of three terms, are loaded inside their step: there
+// are no registers for more, and at rank 64 the kernel spills 92 to 100 bytes a
+// lane wherever one side is fp32.
 //
-// Bound by the loads' latency at two waves a SIMD, whose accumulators (16 RT x
-// 128 fp32 a wave) leave no room for more.  4096 tokens, 4096 + 12288 bf16
-// columns at rank 32: 30 us and 6.5 us of join, 5.6 TB/s with the parts.  16384
-// tokens, 17408 act8 + 5120 bf16 columns at rank 64, 70% of the tokens with an
+// Bound by the loads' latency at two waves a SIMD (one at rank 128), whose
+// accumulators (16 RT x 128 fp32 a wave) leave no room for more.  4096 tokens,
+// 4096 + 12288 bf16 columns at rank 32: 30 us and 6.5 us of join, 5.6 TB/s with
+// the parts.  16384 tokens, 17408 act8 + 5120 bf16 columns at rank 64, 70% of the tokens with an
 // adapter: 86 us and 11 us, 4.4 TB/s; the matrix cores are busy for 22 us of it,
 // turning codes into values takes as long (each wave splitting all of S by
 // itself: 147 us).  An order of the workgroups that keeps a chunk's columns on

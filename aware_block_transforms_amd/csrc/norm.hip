@@ -14,10 +14,10 @@
 //   p  = g gate w_post,          dY = k1 (p - z mean(p z)),        dR = res t
 // All sums are fp32.
 //
-// Both directions are bound by HBM: every value is read and written once.
-// Forward on 16384 x 5120, y fp32, the rest bf16: 151 us, 5.5 TB/s.  Backward on
-// 4096 x 4096: 51 us and 4 us for the column sums, 4.9 TB/s; a copy of 256 MB
-// moves 5.4 TB/s here, one of 1 GiB 5.0.  One row of 4096 takes 3.2 us, a turn
+// Both directions read and write every value once, and large calls up to 8192
+// columns are bound by HBM.  Forward on 16384 x 5120, y fp32, the rest bf16: 151
+// us, 5.5 TB/s.  Backward on 4096 x 4096: 50 us and 5 us for the column sums, 4.9
+// TB/s; a copy of 256 MB moves 5.4 TB/s here, one of 1 GiB 5.0.  One row of 4096 takes 3.2 us, a turn
 // through memory for the loads, one for the weights, and the launch.  A
 // workgroup owns a row, a thread VPT pieces of eight values of it, which stay
 // in registers between the two means.  In the backward kernel a workgroup
@@ -182,7 +182,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int gate_kin
 // column read the last columns again, and tensors that the caller left out are
 // read as one that is there and replaced by zeros, not skipped by a branch.
 // Where a branch or a weight load cut the row's loads off, 4096 x 4096 took 71 us
-// against 59 with as many workgroups.  What the threads past the last column
+// against 59 with as many workgroups.  Five variants of 1024 threads with an fp32
+// r spill 12 to 40 bytes a lane (rows of 4104 to 8192 columns; 4096 x 8192 with bf16 r 114
+// us, a copy 100).  What the threads past the last column
 // would add to a row's sums is dropped by a select on the sum: a factor of zero
 // would make NaN of a row whose gradient holds an infinity there.
 template <class Y, class R, class U, int MAXT, int GATE>
@@ -319,8 +321,11 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a, const float*
 }
 
 // The same for rows above 8192 columns, VPT pieces a thread.  A row stays in
-// registers as it lies in memory and is widened where it is used; even so the
-// widest spill.
+// registers as it lies in memory and is widened where it is used.  Even so every
+// variant spills, 84 to 276 bytes a lane with two pieces and 380 to 808 with four;
+// nor is a row loaded ahead.  That is what bounds it: 4096 x 12288, y fp32, the
+// rest bf16, 326 us, 4096 x 16384 387 and 4096 x 17408 795, where a copy of the
+// bytes takes 151, 203 and 223.
 template <class Y, class R, class U, int VPT, int MAXT, int GATE>
 __global__ __launch_bounds__(MAXT) void norm_bwd_wide_kernel(NormArgs a, const U* __restrict__ du,
                                                         const R* drout, const Y* __restrict__ y,
@@ -508,9 +513,12 @@ __global__ __launch_bounds__(1024) void norm_cols_kernel(int d, int parts, const
 constexpr int kMaxD = 24576;
 
 // Pieces of eight values per thread of the forward kernel.  Few rows: one, up to
-// 8192 columns, since only the number of waves hides latency there (one row of
-// 4096: 3.2 against 4.1 us).  Many: two, whose loads are in flight together
-// (16384 rows of 5120: 156 against 171 us), four past 16384 columns.
+// 8192 columns, since only the number of waves hides latency there.  Many: two,
+// whose loads are in flight together, four past 16384 columns.  One against two
+// pieces in us, y fp32, the rest bf16, at 1, 256, 512, 1024 and 2048 rows: 4096
+// columns 3.2/3.9, 4.1/4.7, 5.1/5.6, 8.5/8.4, 16.0/14.5; 5120 columns 3.6/4.1,
+// 4.7/5.2, 6.2/6.3, 12.1/10.0, 20.2/19.8; 8192 columns 4.0/4.1, 5.7/5.7, 9.0/8.4,
+// 17.3/14.7, 28.8/27.3.  16384 rows of 5120: 171/156.
 int fwd_vpt(int n, int d) { return n < 512 && d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
 
 // The backward kernel's: one up to 8192 columns.  Wider rows take more per

@@ -11,7 +11,6 @@
 namespace wush {
 
 using f32x4 = float __attribute__((ext_vector_type(4)));
-using f32x8 = float __attribute__((ext_vector_type(8)));
 using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
